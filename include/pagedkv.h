@@ -86,6 +86,8 @@ typedef enum pkv_status {
                                       output is undefined (the kernel drained its own copies and ended) */
 #define PKV_DEVERR_SCHEDULE 0x10u  /* the decode workspace was not zero-filled before its first use: that
                                       launch's result is wrong (the workspace is zeroed again) */
+#define PKV_DEVERR_POSITION 0x20u  /* position outside the rotation table: the token was left out (no row of
+                                      it was written) */
 
 /*
  * paged_kv_append -- write the K/V of new tokens into their cache slots.
@@ -516,6 +518,112 @@ pkv_status paged_attention_decode_int8(const void* q, const uint8_t* kv_cache, c
                                        int32_t num_blocks, float scale, int32_t n_q_heads, int32_t n_kv_heads,
                                        int32_t head_dim, int32_t block_size, void* out, pkv_dtype dtype,
                                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Rotary position embedding on the way into the cache.
+ *
+ * paged_kv_append_rope -- rotate the new tokens' queries and keys by their
+ * positions and append keys and values: for every token i with p =
+ * positions[i], c and s the cosines and sines of row p of `cos_sin`,
+ *   (x_a, x_b) -> (x_a c_j - x_b s_j, x_b c_j + x_a s_j)
+ * for the rot_dim / 2 pairs j of every query and key head, where (a, b) =
+ * (j, j + rot_dim / 2), or (2 j, 2 j + 1) if `interleaved`; dims from rot_dim
+ * on are copied.  Then q_out[i] = rotated q[i], and for s = slot_mapping[i] >= 0
+ *   k_cache[s / block_size][h][s % block_size] = rotated k[i][h], v_cache likewise v[i][h]
+ * with paged_kv_append's slot rules (a padding token's query is rotated all
+ * the same).  Each product and each sum is rounded to fp32, the result once to
+ * the dtype.  A position outside [0, max_positions) sets PKV_DEVERR_POSITION:
+ * that token's q_out and cache rows are left as they were.
+ *
+ *   q, k, v      : device, heads [n_heads][head_dim] of one token contiguous;
+ *                  token i starts at element i * {q,k,v}_stride, so that views
+ *                  of one projection's packed output are taken as they are.
+ *                  16-byte aligned, strides a multiple of 16 bytes.  q NULL
+ *                  (and n_q_heads 0): no queries
+ *   q_out        : device, token i at element i * q_out_stride; may be q (with
+ *                  q's stride): the rotation then is in place.  May overlap
+ *                  nothing else
+ *   positions    : device, int64 [num_tokens]
+ *   cos_sin      : device, fp32 [max_positions][rot_dim]: rot_dim / 2 cosines,
+ *                  then rot_dim / 2 sines; 16-byte aligned
+ *   rot_dim      : a multiple of 16, 16 .. head_dim
+ *   head_dim     : a multiple of 16
+ *   dtype        : f32, f16 or bf16, of q, k, v, q_out and the caches
+ */
+pkv_status paged_kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const int64_t* positions, const float* cos_sin,
+                                int64_t max_positions, int32_t rot_dim, int32_t interleaved,
+                                const int64_t* slot_mapping, int32_t num_tokens, void* k_cache, void* v_cache,
+                                int32_t num_blocks, int32_t block_size, int32_t n_q_heads, int32_t n_kv_heads,
+                                int32_t head_dim, void* q_out, int64_t q_out_stride, pkv_dtype dtype, void* stream);
+
+/* ------------------------------------------------------------------------
+ * FP8 paged KV cache: e4m3 codes with one scale for each block, kv head and K
+ * or V (block_size 16, head_dim 64 or 128).
+ *
+ *   kv_cache  : [num_blocks][n_kv_heads][2][block_size][head_dim] e4m3 codes (K,
+ *               then V), 16-byte aligned
+ *   kv_scales : fp32 [num_blocks][n_kv_heads][2], 8-byte aligned; the value of
+ *               a code is code * scale
+ *
+ * paged_kv_append_fp8 -- quantise and write the K/V of new tokens.  For each
+ * (block, kv head, K or V) that the call writes, with T its tokens there:
+ *   need  = the smallest power of two with max |x| <= 448 need over the finite
+ *           x of T, within [2^-48, 2^48] (the code of a magnitude past that and
+ *           of an infinity is +-448; NaN stays NaN)
+ *   scale = need if T holds the block's offset 0, else max(scale, need)
+ *   code  = e4m3(x / scale), nearest even, for the tokens of T; the codes of
+ *           the block's other tokens are rounded to the new scale where it grew
+ * A token at offset 0 starts its block anew: it takes the block's old scale and
+ * tokens away (tokens not of this call become 0).  A block fills from offset 0
+ * on, so nothing that lives is lost; rewriting offset 0 of a block in use
+ * does lose the block's other tokens.
+ * Slots as paged_kv_append (a negative one is padding).  The tokens of one
+ * block have to be consecutive in the call, in any order, with no padding
+ * between them (a step's one token per sequence and a prompt's tokens in order
+ * are); of two with the same slot the last counts.  A block whose tokens come
+ * in two places of one call is undefined.
+ *
+ *   k, v : device, f32, f16 or bf16 (`dtype`), strides as paged_kv_append_rope
+ */
+pkv_status paged_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, pkv_dtype dtype,
+                               const int64_t* slot_mapping, int32_t num_tokens, uint8_t* kv_cache, float* kv_scales,
+                               int32_t num_blocks, int32_t block_size, int32_t n_kv_heads, int32_t head_dim,
+                               void* stream);
+
+/* paged_kv_append_rope into the FP8 cache: q_out as there; keys are rotated in
+ * fp32 and quantised without an intermediate rounding to the dtype. */
+pkv_status paged_kv_append_rope_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, const int64_t* positions, const float* cos_sin,
+                                    int64_t max_positions, int32_t rot_dim, int32_t interleaved,
+                                    const int64_t* slot_mapping, int32_t num_tokens, uint8_t* kv_cache,
+                                    float* kv_scales, int32_t num_blocks, int32_t block_size, int32_t n_q_heads,
+                                    int32_t n_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride,
+                                    pkv_dtype dtype, void* stream);
+
+/* paged_kv_copy_blocks for the FP8 cache: codes and scales of whole blocks. */
+pkv_status paged_kv_copy_blocks_fp8(uint8_t* kv_cache, float* kv_scales, const int32_t* src_blocks,
+                                    const int32_t* dst_blocks, int32_t n_pairs, int32_t num_blocks,
+                                    int32_t block_size, int32_t n_kv_heads, int32_t head_dim, void* stream);
+
+/*
+ * paged_attention_decode_fp8 -- paged_attention_decode, or with q_len > 1
+ * paged_attention_decode_mq, over the FP8 cache: K_j and V_j are codes times
+ * their block's scales.
+ *
+ *   q, out    : device, [batch][q_len][n_q_heads][head_dim], f16 or bf16
+ *   q_len     : 1 .. 16, the last tokens of every context; query i sees tokens
+ *               j < context_lens[b] - q_len + i + 1
+ *   workspace : paged_attention_fp8_workspace_size() bytes, or NULL
+ */
+pkv_status paged_attention_fp8_workspace_size(int32_t batch, int32_t q_len, int32_t n_q_heads, int32_t n_kv_heads,
+                                              int32_t head_dim, size_t* bytes);
+pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, const float* kv_scales,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, int32_t batch, int32_t q_len, int32_t num_blocks,
+                                      float scale, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                      int32_t block_size, void* out, pkv_dtype dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream);
 
 /*
  * pkv_get_device_error -- synchronise `stream`, then read and clear the

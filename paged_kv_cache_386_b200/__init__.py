@@ -12,6 +12,8 @@ Tensors are torch CUDA tensors in the library's layout:
 * ``block_tables``: int32 ``[batch, max_blocks_per_seq]``
 * ``context_lens``: int32 ``[batch]``
 * ``slot_mapping``: int64 ``[num_tokens]``; ``k``, ``v``: ``[num_tokens, n_kv_heads, head_dim]``
+* FP8 cache: ``kv_cache`` float8_e4m3fn ``[num_blocks, n_kv_heads, 2, 16, head_dim]`` (K, then V) and
+  ``kv_scales`` float32 ``[num_blocks, n_kv_heads, 2]``
 """
 
 from __future__ import annotations
@@ -27,8 +29,11 @@ __all__ = [
     "paged_attention_workspace_size", "paged_kv_copy_blocks", "BlockManager", "pkv_bm_hash_blocks",
     "paged_kv_append_int8", "paged_attention_decode_int8", "int8_cache",
     "paged_attention_decode_mq", "paged_attention_mq_workspace_size",
+    "paged_kv_append_rope", "rotary_table", "fp8_cache", "paged_kv_append_fp8", "paged_kv_append_rope_fp8",
+    "paged_kv_copy_blocks_fp8", "paged_attention_decode_fp8", "paged_attention_fp8_workspace_size",
     "pkv_get_device_error", "pkv_status_string", "pkv_version", "PagedKVError", "library_path",
-    "DEVERR_BLOCK_ID", "DEVERR_CONTEXT", "DEVERR_SLOT", "DEVERR_TIMEOUT", "DEVERR_SCHEDULE", "new_workspace",
+    "DEVERR_BLOCK_ID", "DEVERR_CONTEXT", "DEVERR_SLOT", "DEVERR_TIMEOUT", "DEVERR_SCHEDULE",
+    "DEVERR_POSITION", "new_workspace",
 ]
 
 _LIB_PATH = Path(__file__).resolve().parent / "libpagedkv.so"
@@ -39,6 +44,7 @@ _DTYPE = {torch.float32: PKV_F32, torch.float16: PKV_F16, torch.bfloat16: PKV_BF
 PKV_OK = 0
 PKV_ERR_INVALID_ARG, PKV_ERR_NO_BLOCKS = 1, 6
 DEVERR_BLOCK_ID, DEVERR_CONTEXT, DEVERR_SLOT, DEVERR_TIMEOUT, DEVERR_SCHEDULE = 0x1, 0x2, 0x4, 0x8, 0x10
+DEVERR_POSITION = 0x20
 
 
 class PagedKVError(RuntimeError):
@@ -126,6 +132,21 @@ def _load() -> ctypes.CDLL:
                                                 ctypes.c_int, p, sz, p]
     lib.paged_attention_decode_int8.restype = ctypes.c_int
     i64, u64 = ctypes.c_int64, ctypes.c_uint64
+    tok = [p, i64, p, i64]  # k, v and their token strides
+    rope = [p, p, i64, i32, i32, p, i32]  # positions, table, its rows, rot_dim, interleaved, slots, tokens
+    lib.paged_kv_append_rope.argtypes = [p, i64] + tok + rope + [p, p, i32, i32, i32, i32, i32, p, i64, ctypes.c_int, p]
+    lib.paged_kv_append_rope.restype = ctypes.c_int
+    lib.paged_kv_append_fp8.argtypes = tok + [ctypes.c_int, p, i32, p, p, i32, i32, i32, i32, p]
+    lib.paged_kv_append_fp8.restype = ctypes.c_int
+    lib.paged_kv_append_rope_fp8.argtypes = lib.paged_kv_append_rope.argtypes
+    lib.paged_kv_append_rope_fp8.restype = ctypes.c_int
+    lib.paged_kv_copy_blocks_fp8.argtypes = [p, p, p, p, i32, i32, i32, i32, i32, p]
+    lib.paged_kv_copy_blocks_fp8.restype = ctypes.c_int
+    lib.paged_attention_fp8_workspace_size.argtypes = [i32, i32, i32, i32, i32, ctypes.POINTER(sz)]
+    lib.paged_attention_fp8_workspace_size.restype = ctypes.c_int
+    lib.paged_attention_decode_fp8.argtypes = [p, p, p, p, i32, p, i32, i32, i32, f32, i32, i32, i32, i32, p,
+                                               ctypes.c_int, p, sz, p]
+    lib.paged_attention_decode_fp8.restype = ctypes.c_int
     for name, args in (("pkv_bm_create", [i32, i32, i32, ctypes.POINTER(p)]),
                        ("pkv_bm_hash_blocks", [p, i64, i32, u64, p]),
                        ("pkv_bm_add_sequence", [p, i64, i64, p, ctypes.POINTER(i64)]),
@@ -579,4 +600,209 @@ def paged_attention_decode_mq(q, k_cache, v_cache, block_tables, context_lens, s
             block_tables.shape[1], _dev(context_lens, "context_lens"), B, q_len, num_blocks, float(scale), n_q,
             n_kv, d, bs, _dev(out, "out"), _DTYPE[q.dtype], ws_ptr, ws_bytes, _stream(stream, q.device)),
             "paged_attention_decode_mq")
+    return out
+
+
+def rotary_table(max_positions: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Cosines and sines for the rotating appends: float32 ``[max_positions,
+    rot_dim]``, row p the cosines of ``p * theta ** (-2 j / rot_dim)`` for
+    ``j < rot_dim / 2``, then the sines (angles in float64, rounded once)."""
+    if max_positions <= 0 or rot_dim <= 0 or rot_dim % 2:
+        raise ValueError("max_positions must be positive and rot_dim positive and even")
+    j = torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device)
+    angle = torch.arange(max_positions, dtype=torch.float64, device=device)[:, None] * theta ** (-j / rot_dim)
+    return torch.cat((angle.cos(), angle.sin()), 1).float()
+
+
+def _heads(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """Pointer and token stride (elements) of ``[num_tokens, heads, head_dim]``
+    whose heads are contiguous within a token."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    n, h, d = t.shape
+    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+        raise ValueError(f"{name}: the heads of one token must be contiguous")
+    return t.data_ptr(), (t.stride(0) if n > 1 else h * d)
+
+
+def _check_new_tokens(k, v, slot_mapping, n_kv: int, d: int) -> None:
+    if k.dim() != 3 or tuple(k.shape[1:]) != (n_kv, d) or tuple(v.shape) != tuple(k.shape):
+        raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim] with the cache's heads")
+    if k.dtype not in _DTYPE or v.dtype != k.dtype:
+        raise ValueError("k and v must both be float32, float16 or bfloat16")
+    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (k.shape[0],):
+        raise ValueError("slot_mapping must be int64 [num_tokens]")
+
+
+def _check_rope(k, positions, cos_sin, q, q_out) -> None:
+    if positions.dtype != torch.int64 or tuple(positions.shape) != (k.shape[0],):
+        raise ValueError("positions must be int64 [num_tokens]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_positions, rot_dim] (rotary_table)")
+    if q is None:
+        if q_out is not None:
+            raise ValueError("q_out without q")
+        return
+    if q.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or q.dtype != k.dtype:
+        raise ValueError("q must be [num_tokens, n_q_heads, head_dim] of k's dtype")
+    if q_out is not None and (tuple(q_out.shape) != tuple(q.shape) or q_out.dtype != q.dtype):
+        raise ValueError("q_out must have q's shape and dtype")
+
+
+def _empty_for(like: torch.Tensor, stream) -> torch.Tensor:
+    """A contiguous output that belongs to the stream that writes it."""
+    if stream is None:
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+
+
+def _append_rope(entry: str, k, v, positions, cos_sin, slot_mapping, cache, scales, n_blocks, q, q_out, interleaved,
+                 block_size, stream):
+    lib = _load()
+    n_kv, d = k.shape[1:]
+    _same_device(cache.device, k, v, positions, cos_sin, slot_mapping, scales, q, q_out)
+    with torch.cuda.device(cache.device):
+        kp, ks = _heads(k, "k")
+        vp, vs = _heads(v, "v")
+        qp, qs, op, os_, n_q = None, 0, None, 0, 0
+        if q is not None:
+            if q_out is None:
+                q_out = _empty_for(q, stream)
+            qp, qs = _heads(q, "q")
+            op, os_ = _heads(q_out, "q_out")
+            n_q = q.shape[1]
+        _check(getattr(lib, entry)(
+            qp, qs, kp, ks, vp, vs, _dev(positions, "positions"), _dev(cos_sin, "cos_sin"), cos_sin.shape[0],
+            cos_sin.shape[1], int(bool(interleaved)), _dev(slot_mapping, "slot_mapping"), k.shape[0],
+            _dev(cache, "cache"), _dev(scales, "cache"), n_blocks, block_size, n_q, n_kv, d, op, os_,
+            _DTYPE[k.dtype], _stream(stream, cache.device)), entry)
+    return q_out
+
+
+def paged_kv_append_rope(k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q=None, q_out=None,
+                         interleaved: bool = False, block_size: int = 16, stream=None):
+    """Rotate ``k[i]`` (and ``q[i]``) by position ``positions[i]`` and write the
+    rotated key and ``v[i]`` into slot ``slot_mapping[i]`` of the caches (in
+    place).  ``cos_sin`` is a :func:`rotary_table`; its width is the number of
+    rotated dims, paired (j, j + width / 2), or (2 j, 2 j + 1) if
+    ``interleaved``.  ``k``, ``v`` and ``q`` may be views of one packed
+    projection (heads of a token contiguous).  Returns the rotated queries in
+    ``q_out`` (a new tensor by default; ``q_out=q`` rotates in place), or None
+    without ``q``."""
+    num_blocks, n_kv, bs, d = k_cache.shape
+    if bs != block_size or tuple(v_cache.shape) != tuple(k_cache.shape):
+        raise ValueError("cache shapes disagree")
+    _check_new_tokens(k, v, slot_mapping, n_kv, d)
+    if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
+        raise ValueError("the caches must have k's dtype")
+    _check_rope(k, positions, cos_sin, q, q_out)
+    return _append_rope("paged_kv_append_rope", k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, num_blocks,
+                        q, q_out, interleaved, bs, stream)
+
+
+def fp8_cache(num_blocks: int, n_kv_heads: int, head_dim: int, device="cuda"):
+    """An empty FP8 cache ``(kv_cache, kv_scales)``: codes 0, scales 1."""
+    kv = torch.zeros((num_blocks, n_kv_heads, 2, 16, head_dim), dtype=torch.uint8, device=device)
+    return kv.view(torch.float8_e4m3fn), torch.ones((num_blocks, n_kv_heads, 2), dtype=torch.float32, device=device)
+
+
+def _fp8_shape(kv_cache, kv_scales, block_size: int):
+    if kv_cache.dtype != torch.float8_e4m3fn or kv_cache.dim() != 5 or kv_cache.shape[2] != 2:
+        raise ValueError("kv_cache must be float8_e4m3fn [num_blocks, n_kv_heads, 2, 16, head_dim]")
+    num_blocks, n_kv, _, bs, d = kv_cache.shape
+    if bs != block_size:
+        raise ValueError("block size disagrees with kv_cache")
+    if kv_scales.dtype != torch.float32 or tuple(kv_scales.shape) != (num_blocks, n_kv, 2):
+        raise ValueError("kv_scales must be float32 [num_blocks, n_kv_heads, 2]")
+    return num_blocks, n_kv, d
+
+
+def paged_kv_append_fp8(k, v, slot_mapping, kv_cache, kv_scales, block_size: int = 16, stream=None) -> None:
+    """Quantise ``k[i]``, ``v[i]`` into slot ``slot_mapping[i]`` of the FP8 cache
+    (in place): e4m3 codes with one power-of-two scale for each block, kv head
+    and K or V, which grows with what is appended (its rules, and which tokens
+    of a call have to be consecutive, in include/pagedkv.h)."""
+    lib = _load()
+    num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
+    _check_new_tokens(k, v, slot_mapping, n_kv, d)
+    _same_device(kv_cache.device, k, v, slot_mapping, kv_scales)
+    with torch.cuda.device(kv_cache.device):
+        kp, ks = _heads(k, "k")
+        vp, vs = _heads(v, "v")
+        _check(lib.paged_kv_append_fp8(kp, ks, vp, vs, _DTYPE[k.dtype], _dev(slot_mapping, "slot_mapping"),
+                                       k.shape[0], _dev(kv_cache, "kv_cache"), _dev(kv_scales, "kv_scales"),
+                                       num_blocks, block_size, n_kv, d, _stream(stream, kv_cache.device)),
+               "paged_kv_append_fp8")
+
+
+def paged_kv_append_rope_fp8(k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales, q=None, q_out=None,
+                             interleaved: bool = False, block_size: int = 16, stream=None):
+    """paged_kv_append_rope into the FP8 cache (keys are quantised from their
+    fp32 rotation); returns the rotated queries as there."""
+    num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
+    _check_new_tokens(k, v, slot_mapping, n_kv, d)
+    _check_rope(k, positions, cos_sin, q, q_out)
+    return _append_rope("paged_kv_append_rope_fp8", k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales,
+                        num_blocks, q, q_out, interleaved, block_size, stream)
+
+
+def paged_kv_copy_blocks_fp8(kv_cache, kv_scales, src_blocks, dst_blocks, block_size: int = 16, stream=None) -> None:
+    """paged_kv_copy_blocks for the FP8 cache: codes and scales of whole blocks."""
+    lib = _load()
+    num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
+    if src_blocks.dtype != torch.int32 or dst_blocks.dtype != torch.int32 or src_blocks.shape != dst_blocks.shape:
+        raise ValueError("src_blocks and dst_blocks must be int32 of one shape")
+    n = src_blocks.numel()
+    if n == 0:
+        return
+    _same_device(kv_cache.device, kv_scales, src_blocks, dst_blocks)
+    with torch.cuda.device(kv_cache.device):
+        _check(lib.paged_kv_copy_blocks_fp8(_dev(kv_cache, "kv_cache"), _dev(kv_scales, "kv_scales"),
+                                            _dev(src_blocks, "src_blocks"), _dev(dst_blocks, "dst_blocks"), n,
+                                            num_blocks, block_size, n_kv, d, _stream(stream, kv_cache.device)),
+               "paged_kv_copy_blocks_fp8")
+
+
+def paged_attention_fp8_workspace_size(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
+                                       device=None) -> int:
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(device):
+        _check(_load().paged_attention_fp8_workspace_size(batch, q_len, n_q_heads, n_kv_heads, head_dim,
+                                                          ctypes.byref(out)), "paged_attention_fp8_workspace_size")
+    return int(out.value)
+
+
+def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_lens, scale: float, out=None,
+                               workspace=None, block_size: int = 16, stream=None):
+    """paged_attention_decode over the FP8 cache.  ``q`` is ``[batch, n_q, d]``,
+    or ``[batch, q_len, n_q, d]`` for several queries per sequence (query i sees
+    its context up to position ``ctx - q_len + i``), float16 or bfloat16.
+    ``workspace``: :func:`new_workspace` of paged_attention_fp8_workspace_size
+    bytes, for one call at a time.  Returns ``out`` (shape and dtype of q)."""
+    lib = _load()
+    num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
+    if q.dim() not in (3, 4) or q.shape[-1] != d or q.dtype not in _DTYPE:
+        raise ValueError("q must be [batch, n_q, d] or [batch, q_len, n_q, d] with the cache's head_dim")
+    B, q_len, n_q = (q.shape[0], 1, q.shape[1]) if q.dim() == 3 else tuple(q.shape[:3])
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError("block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+        raise ValueError("block_tables must be [batch, max_blocks_per_seq] and context_lens [batch]")
+    if out is None:
+        out = _empty_for(q, stream)
+    if out.dtype != q.dtype or tuple(out.shape) != tuple(q.shape) or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's dtype and shape")
+    _same_device(q.device, kv_cache, kv_scales, out, block_tables, context_lens, workspace)
+    ws_ptr, ws_bytes = None, 0
+    if workspace is not None:
+        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    with torch.cuda.device(q.device):
+        _check(lib.paged_attention_decode_fp8(
+            _dev(q, "q"), _dev(kv_cache, "kv_cache"), _dev(kv_scales, "kv_scales"),
+            _dev(block_tables, "block_tables"), block_tables.shape[1], _dev(context_lens, "context_lens"), B, q_len,
+            num_blocks, float(scale), n_q, n_kv, d, block_size, _dev(out, "out"), _DTYPE[q.dtype], ws_ptr, ws_bytes,
+            _stream(stream, q.device)), "paged_attention_decode_fp8")
     return out

@@ -9,6 +9,8 @@
 #include "pkv_kernels.cuh"
 #include "pkv_prefix.cuh"
 #include "pkv_prefix_tc.cuh"
+#include "pkv_append_f8.cuh"
+#include "pkv_decode_f8.cuh"
 
 namespace pkv {
 namespace {
@@ -990,3 +992,5 @@ pkv_status pkv_get_device_error(void* stream, uint32_t* flags) {
 }
 
 }  // extern "C"
+
+#include "pkv_api_f8.cuh"

@@ -1,0 +1,251 @@
+// pkv_api_f8.cuh -- C ABI of the rotating append and of the FP8 cache (part of
+// pkv_api.cu's translation unit).
+#pragma once
+
+namespace pkv {
+namespace {
+
+// Checks of the new tokens' inputs that the rotating and the FP8 append share;
+// fills the inputs of `p`.  Strides are in elements.
+pkv_status rope_append_params(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, pkv_dtype dtype, const int64_t* positions, const float* cos_sin,
+                              int64_t max_positions, int32_t rot_dim, int32_t interleaved,
+                              const int64_t* slot_mapping, int32_t num_tokens, int32_t num_blocks,
+                              int32_t block_size, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                              void* q_out, int64_t q_out_stride, RopeAppendParams* p) {
+  if (num_tokens < 0 || num_blocks <= 0 || block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0 || n_q_heads < 0 ||
+      rot_dim < 0 || rot_dim > head_dim || (interleaved != 0 && interleaved != 1))
+    return PKV_ERR_INVALID_ARG;
+  const int es = elem_bytes(dtype);
+  if (es == 0 || block_size != kBlockTokens || head_dim % 16 != 0 || rot_dim % 16 != 0) return PKV_ERR_UNSUPPORTED;
+  const int64_t kv_row = static_cast<int64_t>(n_kv_heads) * head_dim, q_row = static_cast<int64_t>(n_q_heads) * head_dim;
+  if (kv_row > INT32_MAX || q_row > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_tokens) * (head_dim / 16) > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  *p = {};
+  if (num_tokens == 0) return PKV_OK;
+  if (!k || !v || !slot_mapping || (n_q_heads > 0) != (q != nullptr) || (n_q_heads > 0 && !q_out))
+    return PKV_ERR_INVALID_ARG;
+  if (rot_dim > 0 && (!positions || !cos_sin || max_positions <= 0)) return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k) || !aligned16(v) || !aligned16(q) || !aligned16(q_out) || !aligned16(cos_sin) ||
+      (reinterpret_cast<uintptr_t>(slot_mapping) & 7u) || (reinterpret_cast<uintptr_t>(positions) & 7u))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t strides[4] = {q_stride, k_stride, v_stride, q_out_stride};
+  for (int i = 0; i < 4; ++i)
+    if (strides[i] < 0 || strides[i] > INT64_MAX / 8 || (strides[i] * es) % 16 != 0) return PKV_ERR_INVALID_ARG;
+  if (num_tokens > 1 && q && q_out_stride < q_row) return PKV_ERR_INVALID_ARG;  // rows would overlap
+  if (num_tokens > 1 && q && q_out == q && q_out_stride != q_stride) return PKV_ERR_INVALID_ARG;
+  p->q = static_cast<const uint8_t*>(q);
+  p->k = static_cast<const uint8_t*>(k);
+  p->v = static_cast<const uint8_t*>(v);
+  p->q_out = static_cast<uint8_t*>(q_out);
+  p->q_stride = q_stride * es;
+  p->k_stride = k_stride * es;
+  p->v_stride = v_stride * es;
+  p->q_out_stride = q_out_stride * es;
+  p->slot_mapping = slot_mapping;
+  p->num_slots = static_cast<int64_t>(num_blocks) * block_size;
+  p->rope = {cos_sin, positions, max_positions, rot_dim, interleaved};
+  p->num_tokens = num_tokens;
+  p->n_q = n_q_heads;
+  p->n_kv = n_kv_heads;
+  p->head_dim = head_dim;
+  return PKV_OK;
+}
+
+// Heads that one thread of the rotation walks, sharing a token's cosines
+// and sines: as many as leave about two threads for every one the device
+// holds, at most 8.
+int rope_heads_per_thread(int64_t columns, int heads, int sm_count) {
+  const int64_t want = static_cast<int64_t>(sm_count) * 2048;
+  for (int hp = 8; hp > 1; hp /= 2)
+    if (columns * ((heads + hp - 1) / hp) >= want) return hp;
+  return 1;
+}
+
+template <int DT>
+pkv_status launch_append_f8(const AppendF8Params& p, unsigned grid, cudaStream_t s) {
+  if (p.rp.head_dim == 64)
+    pkv_append_f8_kernel<DT, 64><<<grid, 256, 0, s>>>(p);
+  else
+    pkv_append_f8_kernel<DT, 128><<<grid, 256, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+// paged_kv_append_fp8 and paged_kv_append_rope_fp8 (rot_dim 0: no rotation, no queries).
+pkv_status append_f8(const RopeAppendParams& rp, pkv_dtype dtype, uint8_t* kv_cache, float* kv_scales,
+                     cudaStream_t s) {
+  if (rp.num_tokens == 0) return PKV_OK;
+  if (!kv_cache || !kv_scales || !aligned16(kv_cache) || (reinterpret_cast<uintptr_t>(kv_scales) & 7u))
+    return PKV_ERR_INVALID_ARG;
+  DeviceInfo di;
+  if (device_info(&di) != PKV_OK) return PKV_ERR_CUDA;
+  AppendF8Params p;
+  p.rp = rp;
+  p.kv = kv_cache;
+  p.scales = kv_scales;
+  const int64_t heads2 = 2 * static_cast<int64_t>(rp.n_kv);
+  // A token a warp while all of them fit the device at once (a decode step:
+  // every token its own run); else 16, so that a prompt's warps are not
+  // mostly ones without a run start.
+  p.tokens_per_warp = rp.num_tokens * heads2 <= static_cast<int64_t>(di.sm_count) * 64 ? 1 : 16;
+  p.token_chunks = (rp.num_tokens + p.tokens_per_warp - 1) / p.tokens_per_warp;
+  const int64_t kv_ctas = (p.token_chunks * heads2 + 7) / 8;
+  const int64_t columns = static_cast<int64_t>(rp.num_tokens) * (rp.head_dim / 16);
+  int64_t groups = 0;
+  p.q_ctas = static_cast<int32_t>((columns + 255) / 256);
+  if (rp.n_q > 0) {
+    p.rp.heads_per_thread = rope_heads_per_thread(columns, rp.n_q, di.sm_count);
+    groups = (rp.n_q + p.rp.heads_per_thread - 1) / p.rp.heads_per_thread;
+  }
+  const int64_t grid = kv_ctas + groups * p.q_ctas;
+  if (grid > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  p.kv_ctas = static_cast<int32_t>(kv_ctas);
+  switch (dtype) {
+    case PKV_F32: return launch_append_f8<kF32>(p, static_cast<unsigned>(grid), s);
+    case PKV_F16: return launch_append_f8<kF16>(p, static_cast<unsigned>(grid), s);
+    default: return launch_append_f8<kBF16>(p, static_cast<unsigned>(grid), s);
+  }
+}
+
+}  // namespace
+}  // namespace pkv
+
+extern "C" {
+
+pkv_status paged_kv_append_rope(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                int64_t v_stride, const int64_t* positions, const float* cos_sin,
+                                int64_t max_positions, int32_t rot_dim, int32_t interleaved,
+                                const int64_t* slot_mapping, int32_t num_tokens, void* k_cache, void* v_cache,
+                                int32_t num_blocks, int32_t block_size, int32_t n_q_heads, int32_t n_kv_heads,
+                                int32_t head_dim, void* q_out, int64_t q_out_stride, pkv_dtype dtype, void* stream) {
+  if (rot_dim == 0) return PKV_ERR_INVALID_ARG;
+  RopeAppendParams p;
+  const pkv_status st =
+      rope_append_params(q, q_stride, k, k_stride, v, v_stride, dtype, positions, cos_sin, max_positions, rot_dim,
+                         interleaved, slot_mapping, num_tokens, num_blocks, block_size, n_q_heads, n_kv_heads,
+                         head_dim, q_out, q_out_stride, &p);
+  if (st != PKV_OK || num_tokens == 0) return st;
+  if (!k_cache || !v_cache || !aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
+  p.k_cache = static_cast<uint8_t*>(k_cache);
+  p.v_cache = static_cast<uint8_t*>(v_cache);
+  DeviceInfo di;
+  if (device_info(&di) != PKV_OK) return PKV_ERR_CUDA;
+  const int heads = n_q_heads + 2 * n_kv_heads;
+  const int64_t columns = static_cast<int64_t>(num_tokens) * (head_dim / 16);
+  p.heads_per_thread = rope_heads_per_thread(columns, heads, di.sm_count);
+  const int64_t groups = (heads + p.heads_per_thread - 1) / p.heads_per_thread;
+  if (groups > 65535) return PKV_ERR_UNSUPPORTED;
+  const dim3 grid(static_cast<unsigned>((columns + 255) / 256), static_cast<unsigned>(groups));
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  switch (dtype) {
+    case PKV_F32: pkv_append_rope_kernel<kF32><<<grid, 256, 0, s>>>(p); break;
+    case PKV_F16: pkv_append_rope_kernel<kF16><<<grid, 256, 0, s>>>(p); break;
+    default: pkv_append_rope_kernel<kBF16><<<grid, 256, 0, s>>>(p); break;
+  }
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status paged_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, pkv_dtype dtype,
+                               const int64_t* slot_mapping, int32_t num_tokens, uint8_t* kv_cache, float* kv_scales,
+                               int32_t num_blocks, int32_t block_size, int32_t n_kv_heads, int32_t head_dim,
+                               void* stream) {
+  RopeAppendParams p;
+  const pkv_status st =
+      rope_append_params(nullptr, 0, k, k_stride, v, v_stride, dtype, nullptr, nullptr, 0, 0, 0, slot_mapping,
+                         num_tokens, num_blocks, block_size, 0, n_kv_heads, head_dim, nullptr, 0, &p);
+  if (st != PKV_OK) return st;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  return append_f8(p, dtype, kv_cache, kv_scales, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_kv_append_rope_fp8(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                    int64_t v_stride, const int64_t* positions, const float* cos_sin,
+                                    int64_t max_positions, int32_t rot_dim, int32_t interleaved,
+                                    const int64_t* slot_mapping, int32_t num_tokens, uint8_t* kv_cache,
+                                    float* kv_scales, int32_t num_blocks, int32_t block_size, int32_t n_q_heads,
+                                    int32_t n_kv_heads, int32_t head_dim, void* q_out, int64_t q_out_stride,
+                                    pkv_dtype dtype, void* stream) {
+  if (rot_dim == 0) return PKV_ERR_INVALID_ARG;
+  RopeAppendParams p;
+  const pkv_status st =
+      rope_append_params(q, q_stride, k, k_stride, v, v_stride, dtype, positions, cos_sin, max_positions, rot_dim,
+                         interleaved, slot_mapping, num_tokens, num_blocks, block_size, n_q_heads, n_kv_heads,
+                         head_dim, q_out, q_out_stride, &p);
+  if (st != PKV_OK) return st;
+  if (head_dim != 64 && head_dim != 128) return PKV_ERR_UNSUPPORTED;
+  return append_f8(p, dtype, kv_cache, kv_scales, static_cast<cudaStream_t>(stream));
+}
+
+pkv_status paged_kv_copy_blocks_fp8(uint8_t* kv_cache, float* kv_scales, const int32_t* src_blocks,
+                                    const int32_t* dst_blocks, int32_t n_pairs, int32_t num_blocks,
+                                    int32_t block_size, int32_t n_kv_heads, int32_t head_dim, void* stream) {
+  if (n_pairs < 0 || num_blocks <= 0 || block_size <= 0 || n_kv_heads <= 0 || head_dim <= 0)
+    return PKV_ERR_INVALID_ARG;
+  if (block_size != kBlockTokens || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+  if (n_pairs == 0) return PKV_OK;
+  if (!kv_cache || !kv_scales || !src_blocks || !dst_blocks || !aligned16(kv_cache) ||
+      (reinterpret_cast<uintptr_t>(kv_scales) & 7u) || (reinterpret_cast<uintptr_t>(src_blocks) & 3u) ||
+      (reinterpret_cast<uintptr_t>(dst_blocks) & 3u))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t chunks = static_cast<int64_t>(n_kv_heads) * f8_tile_bytes(head_dim) / 16;
+  if (chunks > INT32_MAX - 1024) return PKV_ERR_UNSUPPORTED;
+  DeviceInfo di;
+  if (device_info(&di) != PKV_OK) return PKV_ERR_CUDA;
+  const CopyF8Params p = {kv_cache,   kv_scales, src_blocks, dst_blocks, n_pairs,
+                          num_blocks, static_cast<int32_t>(chunks), 2 * n_kv_heads};
+  const int grid = n_pairs < di.sm_count * 8 ? n_pairs : di.sm_count * 8;
+  pkv_copy_blocks_f8_kernel<<<grid, 256, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status paged_attention_fp8_workspace_size(int32_t batch, int32_t q_len, int32_t n_q_heads, int32_t n_kv_heads,
+                                              int32_t head_dim, size_t* bytes) {
+  if (!bytes || batch < 0 || q_len < 1 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0)
+    return PKV_ERR_INVALID_ARG;
+  if (q_len > 16 || batch > PKV_MAX_BATCH || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
+  *bytes = 256;
+  return PKV_OK;
+}
+
+pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, const float* kv_scales,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* context_lens, int32_t batch, int32_t q_len, int32_t num_blocks,
+                                      float scale, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                      int32_t block_size, void* out, pkv_dtype dtype, void* workspace,
+                                      size_t workspace_bytes, void* stream) {
+  pkv_status st = check_decode_args(q, kv_cache, kv_cache, block_tables, max_blocks_per_seq, context_lens, batch,
+                                    num_blocks, scale, n_q_heads, n_kv_heads, head_dim, block_size, out, dtype);
+  if (st != PKV_OK) return st;
+  if (q_len < 1) return PKV_ERR_INVALID_ARG;
+  if (q_len > 16 || dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
+  if (batch == 0) return PKV_OK;
+  if (!kv_scales || (reinterpret_cast<uintptr_t>(kv_scales) & 7u)) return PKV_ERR_INVALID_ARG;
+  DecodeF8Params p;
+  p.q = static_cast<const uint16_t*>(q);
+  p.out = static_cast<uint16_t*>(out);
+  p.kv = kv_cache;
+  p.scales = kv_scales;
+  p.block_tables = block_tables;
+  p.context_lens = context_lens;
+  p.max_blocks_per_seq = max_blocks_per_seq;
+  p.batch = batch;
+  p.num_blocks = num_blocks;
+  p.n_q_heads = n_q_heads;
+  p.n_kv_heads = n_kv_heads;
+  p.q_len = q_len;
+  p.gp = heads_per_segment_mq(n_q_heads / n_kv_heads, q_len);
+  p.rows = p.gp * q_len;
+  p.ng = n_q_heads / p.gp;
+  p.bf16 = dtype == PKV_BF16;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  (void)workspace;
+  (void)workspace_bytes;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (head_dim == 64)
+    pkv_decode_f8_kernel<64><<<batch * p.ng, 128, 0, s>>>(p);
+  else
+    pkv_decode_f8_kernel<128><<<batch * p.ng, 128, 0, s>>>(p);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+}  // extern "C"
