@@ -185,11 +185,28 @@ pkv_status encode_cache_map_kgroups(CUtensorMap* map, const void* cache, pkv_dty
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// A block's K and V codes of one kv head in the FP8 cache as one TMA box: dims
+// {head_dim bytes, 32 rows (16 of K, 16 of V), block x kv head}, landing with
+// the swizzle of the row's size.
+pkv_status encode_cache_map_f8(CUtensorMap* map, const void* cache, int num_blocks, int n_kv, int head_dim) {
+  const cuuint64_t row = static_cast<cuuint64_t>(head_dim);
+  const cuuint64_t dims[3] = {row, 2 * kBlockTokens,
+                              static_cast<cuuint64_t>(num_blocks) * static_cast<cuuint64_t>(n_kv)};
+  const cuuint64_t strides[2] = {row, 2 * kBlockTokens * row};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(head_dim), 2 * kBlockTokens, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_CUDA;
+}
+
 // Encoded tensor maps, cached per (kind, base address, dtype, shape): a map
 // depends only on those, so a serving loop that calls with the same caches
 // every step pays the encode once.  A small table with least-recently-used
 // replacement, shared by every device and host thread.
-enum MapKind { kMapBox = 0, kMapTile = 1, kMapKGroups = 2 };
+enum MapKind { kMapBox = 0, kMapTile = 1, kMapKGroups = 2, kMapF8 = 3 };
 struct MapKey {
   const void* base;
   int kind, dtype, num_blocks, n_kv, head_dim;
@@ -223,6 +240,7 @@ pkv_status cached_map(MapKind kind, CUtensorMap* map, const void* cache, pkv_dty
   }
   const pkv_status st = kind == kMapTile      ? encode_cache_map_tile(map, cache, dt, num_blocks, n_kv, head_dim)
                         : kind == kMapKGroups ? encode_cache_map_kgroups(map, cache, dt, num_blocks, n_kv, head_dim)
+                        : kind == kMapF8      ? encode_cache_map_f8(map, cache, num_blocks, n_kv, head_dim)
                                               : encode_cache_map(map, cache, dt, num_blocks, n_kv, head_dim);
   if (st != PKV_OK) return st;
   std::lock_guard<std::mutex> lock(g_map_mutex);

@@ -107,6 +107,39 @@ pkv_status append_f8(const RopeAppendParams& rp, pkv_dtype dtype, uint8_t* kv_ca
   }
 }
 
+// Rows of a segment: all rows of a kv head up to 16, else equal parts.
+void decode_f8_segments(int total_rows, int* nseg, int* rows) {
+  *nseg = (total_rows + 15) / 16;
+  *rows = (total_rows + *nseg - 1) / *nseg;
+}
+
+size_t decode_f8_workspace(int sm_count, int rows, int head_dim) {
+  const size_t records = static_cast<size_t>(sm_count) * (kF8Warps + 2);  // a unit's each, two of each CTA
+  return kF8HeaderBytes + records * rows * (head_dim + 4) * sizeof(float);
+}
+
+template <int D, int NR>
+pkv_status launch_decode_f8(const CUtensorMap& map, DecodeF8Params p, const DeviceInfo& di, cudaStream_t s) {
+  auto kern = pkv_decode_f8_kernel<D, NR>;
+  static bool opted_in[kMaxDevices] = {};
+  int dev = 0;
+  cudaFuncAttributes fa;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PKV_ERR_CUDA;
+  constexpr int kStatic = 1024;  // more than the kernel's static shared memory
+  if (!opted_in[dev]) {
+    if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.sharedSizeBytes > kStatic ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin - kStatic) != cudaSuccess)
+      return PKV_ERR_CUDA;
+    opted_in[dev] = true;
+  }
+  p.stages = kF8MaxStages;
+  auto smem = [&] { return f8_ring_bytes(D, p.stages) + f8_other_bytes(D, NR, p.stages, p.batch); };
+  while (smem() > static_cast<size_t>(di.smem_optin - kStatic)) --p.stages;
+  if (p.stages < NR + 1) return PKV_ERR_UNSUPPORTED;  // a warp's ring holds a record
+  kern<<<di.sm_count, kF8Threads, smem(), s>>>(map, p);
+  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 }  // namespace
 }  // namespace pkv
 
@@ -203,7 +236,11 @@ pkv_status paged_attention_fp8_workspace_size(int32_t batch, int32_t q_len, int3
   if (!bytes || batch < 0 || q_len < 1 || n_q_heads <= 0 || n_kv_heads <= 0 || n_q_heads % n_kv_heads != 0)
     return PKV_ERR_INVALID_ARG;
   if (q_len > 16 || batch > PKV_MAX_BATCH || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
-  *bytes = 256;
+  DeviceInfo di;
+  if (device_info(&di) != PKV_OK) return PKV_ERR_CUDA;
+  int nseg, rows;
+  decode_f8_segments(n_q_heads / n_kv_heads * q_len, &nseg, &rows);
+  *bytes = decode_f8_workspace(di.sm_count, rows, head_dim);
   return PKV_OK;
 }
 
@@ -220,11 +257,14 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
   if (q_len > 16 || dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
   if (batch == 0) return PKV_OK;
   if (!kv_scales || (reinterpret_cast<uintptr_t>(kv_scales) & 7u)) return PKV_ERR_INVALID_ARG;
-  DecodeF8Params p;
+  if (static_cast<int64_t>(num_blocks) * n_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;  // a TMA coordinate
+  DeviceInfo di;
+  if (device_info(&di) != PKV_OK) return PKV_ERR_CUDA;
+  if (static_cast<size_t>(di.sm_count) * sizeof(unsigned int) > kF8HeaderBytes) return PKV_ERR_UNSUPPORTED;
+  DecodeF8Params p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
-  p.kv = kv_cache;
-  p.scales = kv_scales;
+  p.scales = reinterpret_cast<const float2*>(kv_scales);
   p.block_tables = block_tables;
   p.context_lens = context_lens;
   p.max_blocks_per_seq = max_blocks_per_seq;
@@ -233,19 +273,42 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
   p.n_q_heads = n_q_heads;
   p.n_kv_heads = n_kv_heads;
   p.q_len = q_len;
-  p.gp = heads_per_segment_mq(n_q_heads / n_kv_heads, q_len);
-  p.rows = p.gp * q_len;
-  p.ng = n_q_heads / p.gp;
+  p.group = n_q_heads / n_kv_heads;
+  p.total_rows = p.group * q_len;
+  decode_f8_segments(p.total_rows, &p.nseg, &p.rows);
+  p.ng = n_kv_heads * p.nseg;
+  if (static_cast<int64_t>(batch) * max_blocks_per_seq * p.ng > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  p.rec_floats = p.rows * (head_dim + 4);
   p.bf16 = dtype == PKV_BF16;
   p.scale_log2 = scale * 1.4426950408889634f;
-  (void)workspace;
-  (void)workspace_bytes;
+  p.wait_limit_ns = kWaitLimitNs;
+
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const size_t need = decode_f8_workspace(di.sm_count, p.rows, head_dim);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  if (ws && (workspace_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u))) return PKV_ERR_WORKSPACE;
+  CUtensorMap map;
+  st = cached_map(kMapF8, &map, kv_cache, dtype, num_blocks, n_kv_heads, head_dim);
+  if (st != PKV_OK) return st;
+  const bool own = ws == nullptr;
+  if (own) {
+    void* at = nullptr;
+    if (cudaMallocAsync(&at, need, s) != cudaSuccess) return PKV_ERR_CUDA;
+    ws = static_cast<uint8_t*>(at);
+    if (cudaMemsetAsync(ws, 0, kF8HeaderBytes, s) != cudaSuccess) {
+      cudaFreeAsync(ws, s);
+      return PKV_ERR_CUDA;
+    }
+  }
+  p.counters = reinterpret_cast<unsigned int*>(ws);
+  p.unit_recs = reinterpret_cast<float*>(ws + kF8HeaderBytes);
+  p.cta_recs = p.unit_recs + static_cast<size_t>(di.sm_count) * kF8Warps * p.rec_floats;
   if (head_dim == 64)
-    pkv_decode_f8_kernel<64><<<batch * p.ng, 128, 0, s>>>(p);
+    st = p.rows <= 8 ? launch_decode_f8<64, 1>(map, p, di, s) : launch_decode_f8<64, 2>(map, p, di, s);
   else
-    pkv_decode_f8_kernel<128><<<batch * p.ng, 128, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    st = p.rows <= 8 ? launch_decode_f8<128, 1>(map, p, di, s) : launch_decode_f8<128, 2>(map, p, di, s);
+  if (own && cudaFreeAsync(ws, s) != cudaSuccess && st == PKV_OK) st = PKV_ERR_CUDA;
+  return st;
 }
 
 }  // extern "C"

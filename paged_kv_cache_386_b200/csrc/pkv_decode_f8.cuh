@@ -1,128 +1,836 @@
 // pkv_decode_f8.cuh -- decode attention over the FP8 cache (e4m3 codes, one
 // scale for each block, kv head and K or V).
+//
+// Work.  A tile is one (block, kv head): K and V codes, 32 D contiguous
+// bytes.  A segment is the context of one sequence for up to 16 rows (query,
+// head) of one kv head.  The tiles of all segments in order are cut into equal
+// ranges, one per consumer warp ("unit"); W consecutive units are a CTA's.
+// Nothing waits for another CTA: a segment that several warps of one CTA
+// share is merged in shared memory when the CTA is done, one that several CTAs
+// share by the CTA that finishes it last (a counter per CTA where such a
+// segment starts), always in the order of the context, so that the bits do
+// not depend on which CTA that is.
+//
+// Arithmetic of a tile (one warp).  With s_K, s_V the block's scales and
+// e = floor(log2 s_V), f = s_V 2^-e:
+//   S^T = K Q^T            mma m16n8k16 f16: 16 tokens x 8 rows, codes as f16
+//                          (exact), Q as f16 (exact; bf16 rows are first scaled
+//                          by a power of two), fp32 sums
+//   y   = S s_K c + e - m  c = scale log2(e), m the row's reference
+//   O^T += V^T (2^y f)^T   16 dims x 8 rows, codes as f16, weights as f16
+//   l   += 2^y 2^-e
+// so that a block's V scale costs one addition in the exponent, weights are
+// largest where p V is, and out = O / l.  The reference m is 2^7 below the
+// largest p s_V seen and moves only when a weight would pass 2^14: a vote per
+// tile, a reduction over tokens when it moves (at a segment's first tiles),
+// and weights keep f16's full precision down to 2^-21 of the largest.  With
+// f16 data the rounding of the weights (2^-12) is as large as that of the
+// output, so their remainders take a second product.
+//
+// Rows on the n side of the product halve the products for 8 rows or fewer
+// (16 f16 MMAs for a tile of 16 x 128 K and V, not 32) and the accumulators.
+//
+// Bound: HBM, 2 D bytes a token and kv head.  A tile of 4 KiB has to be done
+// every 178 cycles of an SM at the measured copy rate; measured, its 64
+// conversions take 49 of them and its MMAs 33 (2.04 each).  Tensor-memory MMAs
+// on the codes would need Q and P cut into e4m3 pieces and a block-wide softmax
+// over 128 tokens, to relieve pipes that are idle most of the time.
 #pragma once
 
 #include "pkv_append_f8.cuh"
+#include "pkv_prefix_tc.cuh"
 
 namespace pkv {
 
-constexpr int kF8MaxRows = 16;  // (query, head) rows that share a pass over K and V
+constexpr int kF8Warps = 10;                          // consumer warps (units) of a CTA
+constexpr int kF8Threads = (kF8Warps + 1) * 32;       // and one producer warp
+constexpr int kF8MaxStages = 4;                       // ring slots of a warp
+constexpr int kF8MinTiles = 2;                        // tiles that make a unit worth its merge
+constexpr int kF8HeaderBytes = 4096;                  // workspace: a counter per CTA
+constexpr float kF8RefBelow = 7.f, kF8RefSlack = 14.f;
 
 struct DecodeF8Params {
   const uint16_t* q;  // [batch][q_len][n_q][D], f16 or bf16
   uint16_t* out;
-  const uint8_t* kv;
-  const float* scales;
+  const float2* scales;  // [num_blocks][n_kv]
   const int32_t* block_tables;
   const int32_t* context_lens;
+  unsigned int* counters;  // [CTAs], 0 between launches
+  float* unit_recs;        // [units][rec_floats]: a segment that ends inside a unit and began before it
+  float* cta_recs;         // [CTAs][2][rec_floats]: the CTA's share of a segment from before it, of one that goes on
   int32_t max_blocks_per_seq, batch, num_blocks, n_q_heads, n_kv_heads, q_len;
-  int32_t gp;     // query heads per segment
-  int32_t rows;   // gp * q_len
-  int32_t ng;     // segments per sequence
+  int32_t group;       // query heads per kv head
+  int32_t total_rows;  // group * q_len rows of a kv head: row i is query i / group, head i % group
+  int32_t rows;        // rows of a segment (the last one of a kv head may have fewer)
+  int32_t nseg;        // segments of a kv head
+  int32_t ng;          // segments of a sequence, n_kv * nseg
+  int32_t stages;
+  int32_t rec_floats;  // rows * (D + 4)
   int32_t bf16;
   float scale_log2;
+  uint64_t wait_limit_ns;
 };
 
-// One CTA of 128 threads per segment (the rows of one kv head of one
-// sequence): 128 tokens at a time, a thread first owns a token (scores), then
-// a dim (output).
+// 3-D box of one tile: D bytes x 32 rows (16 of K, 16 of V) of one (block, kv head).
+__device__ __forceinline__ void tma_load_3d_hint(void* dst, const CUtensorMap* map, uint64_t* bar, int c2,
+                                                 uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(0), "r"(c2), "l"(policy)
+      : "memory");
+}
+
+__device__ __forceinline__ uint64_t l2_policy_evict_normal() {
+  uint64_t pol;
+  asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(pol));
+  return pol;
+}
+
+__device__ __forceinline__ void cp_async_8(void* dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+
+// One arrival on `bar` (counted in its initial count) when this thread's cp.asyncs so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// Two 16 x 16 byte matrices, transposed: lane (g, t) = (lane / 4, lane % 4)
+// holds bytes 4 t .. 4 t + 3 (rows) of columns g (r0) and g + 8 (r1), then of
+// the second matrix (r2, r3).  Lane l gives row l % 16 of matrix l / 16.
+__device__ __forceinline__ void ldsm_b8_x2_trans(uint32_t addr, uint32_t& r0, uint32_t& r1, uint32_t& r2,
+                                                 uint32_t& r3) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+               : "r"(addr));
+}
+
+// 8 x 8 transpose of packed 16-bit pairs: lane (g, t) holds row g, columns 2 t, 2 t + 1 before and after.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+// Element offset in q and out of row `i` (of the kv head's total_rows).
+__device__ __forceinline__ size_t f8_row_at(const DecodeF8Params& p, int b, int kvh, int i, int D) {
+  const int qi = i / p.group;
+  return ((static_cast<size_t>(b) * p.q_len + qi) * p.n_q_heads + kvh * p.group + (i - qi * p.group)) * D;
+}
+
+// 16-byte chunk c of token row `tok` in a swizzled tile (128-byte rows: c ^
+// row % 8; 64-byte rows: c ^ (row / 2) % 4, the 64-byte swizzle).
 template <int D>
-__global__ void __launch_bounds__(128) pkv_decode_f8_kernel(const DecodeF8Params p) {
-  __shared__ float q_s[kF8MaxRows][D];
-  __shared__ float w_s[kF8MaxRows][128];
-  __shared__ float v_scale[8];
-  __shared__ int block_id[8];
-  __shared__ float red[4];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.ng, hg = blockIdx.x % p.ng;
-  const int kvh = hg * p.gp / (p.n_q_heads / p.n_kv_heads);
-  int ctx = __ldg(p.context_lens + b);
-  const int max_ctx = p.max_blocks_per_seq * kBlockTokens;
-  if (ctx < 0 || ctx > max_ctx || (ctx > 0 && ctx < p.q_len)) {
-    if (tid == 0) flag_error(PKV_DEVERR_CONTEXT);
-    ctx = ctx < 0 || ctx < p.q_len ? 0 : max_ctx;
-  }
-  auto row_at = [&](int r) {
-    return ((static_cast<size_t>(b) * p.q_len + r / p.gp) * p.n_q_heads + hg * p.gp + r % p.gp) * D;
-  };
-  auto to_f = [&](uint16_t h) {
-    float lo, hi;
-    if (p.bf16) unpack2<true>(h, lo, hi); else unpack2<false>(h, lo, hi);
-    return lo;
-  };
-  for (int i = tid; i < p.rows * D; i += 128) q_s[i / D][i % D] = to_f(p.q[row_at(i / D) + i % D]);
-  float o[kF8MaxRows], m[kF8MaxRows], l[kF8MaxRows];
-  for (int r = 0; r < kF8MaxRows; ++r) o[r] = 0.f, m[r] = -INFINITY, l[r] = 0.f;
-  for (int t0 = 0; t0 < ctx; t0 += 128) {
-    __syncthreads();
-    if (tid < 8) {
-      const int j = t0 / kBlockTokens + tid;
-      int id = j * kBlockTokens < ctx ? __ldg(p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq + j) : -2;
-      if (id != -2 && (id < 0 || id >= p.num_blocks)) {
-        flag_error(PKV_DEVERR_BLOCK_ID);
-        id = -1;
+__device__ __forceinline__ uint32_t f8_chunk_at(int tok, int c) {
+  return static_cast<uint32_t>(tok * D + (D == 128 ? c ^ (tok & 7) : c ^ ((tok >> 1) & 3)) * 16);
+}
+
+template <int D, int NR>
+struct F8Consumer {
+  static constexpr int KS = D / 16;    // k-steps of S
+  static constexpr int MT = D / 16;    // 16-dim tiles of O
+  static constexpr int RS = D + 4;     // floats of a record's row: O, m, l, and padding against bank conflicts
+  uint32_t qb[NR][KS][2];
+  float o[NR][MT][4];                  // dims 16 mt + g (+ 8), rows 8 nr + 2 t (+ 1)
+  float m[NR][2], l[NR][2], c[NR][2];  // reference, sum over this lane's tokens, factor of s_K, of those rows
+  int hide[NR][2];                     // tokens at the context's end that the row does not see
+
+  __device__ __forceinline__ void begin(const DecodeF8Params& p, const uint8_t* qbuf, int first_row, int rows,
+                                        int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    constexpr int DL = D / 4;  // consecutive dims of a lane: k-step kk takes 4 of them, K alike
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+      const int row = 8 * nr + g;
+      uint32_t w[DL / 2];
+      const uint4* src = reinterpret_cast<const uint4*>(qbuf + row * D * 2 + t * DL * 2);
+#pragma unroll
+      for (int i = 0; i < DL / 8; ++i) {
+        const uint4 v = row < rows ? src[i] : make_uint4(0u, 0u, 0u, 0u);
+        w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
-      block_id[tid] = id;
-      v_scale[tid] = id >= 0 ? p.scales[(static_cast<size_t>(id) * p.n_kv_heads + kvh) * 2 + 1] : 0.f;
-    }
-    __syncthreads();
-    const int t = t0 + tid, id = block_id[tid / 16];
-    const bool live = id >= 0 && t < ctx;
-    float s[kF8MaxRows];
-    for (int r = 0; r < kF8MaxRows; ++r) s[r] = 0.f;
-    if (live) {
-      const size_t tile = static_cast<size_t>(id) * p.n_kv_heads + kvh;
-      const uint8_t* k = p.kv + tile * f8_tile_bytes(D) + (tid % 16) * D;
-      const float ks = p.scales[tile * 2] * p.scale_log2;
-      for (int e = 0; e < D; e += 2) {
-        float k0, k1;
-        unpack2<false>(f8_unpack2(*reinterpret_cast<const uint16_t*>(k + e)), k0, k1);
-        for (int r = 0; r < p.rows; ++r) s[r] += q_s[r][e] * k0 + q_s[r][e + 1] * k1;
+      float cs = p.scale_log2;
+      if (p.bf16) {
+        // The row's largest magnitude to [2^13, 2^14): what is more than 2^28
+        // times smaller keeps fewer bits.
+        float mx = 0.f;
+#pragma unroll
+        for (int i = 0; i < DL / 2; ++i) {
+          float lo, hi;
+          unpack2<true>(w[i], lo, hi);
+          mx = fmaxf(mx, fmaxf(fabsf(lo), fabsf(hi)));
+        }
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+        const int e = min(max(static_cast<int>(__float_as_uint(mx) >> 23) - 127, -100), 127);
+        // 2^(13 - e) as two factors that are both in range.
+        const int up = 13 - e, u1 = up / 2, u2 = up - u1;
+        const float f1 = __uint_as_float((u1 + 127) << 23), f2 = __uint_as_float((u2 + 127) << 23);
+        const float d1 = __uint_as_float((127 - u1) << 23), d2 = __uint_as_float((127 - u2) << 23);
+#pragma unroll
+        for (int i = 0; i < DL / 2; ++i) {
+          float lo, hi;
+          unpack2<true>(w[i], lo, hi);
+          w[i] = pack2<false>(lo * f1 * f2, hi * f1 * f2);
+        }
+        cs = p.scale_log2 * d1 * d2;
       }
-      for (int r = 0; r < kF8MaxRows; ++r) s[r] *= ks;
-    }
-    for (int r = 0; r < p.rows; ++r) {
-      const bool seen = live && t < ctx - p.q_len + r / p.gp + 1;
-      const float x = seen ? s[r] : -INFINITY;
-      float mx = x;
-      for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-      if (lane == 0) red[warp] = mx;
-      __syncthreads();
-      mx = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-      __syncthreads();
-      const float mn = fmaxf(m[r], mx);
-      const float alpha = m[r] == -INFINITY ? 0.f : exp2f(m[r] - mn);
-      const float w = seen ? exp2f(x - mn) : 0.f;
-      o[r] *= alpha;
-      l[r] = l[r] * alpha + w;
-      m[r] = mn;
-      w_s[r][tid] = w;
-    }
-    __syncthreads();
-    if (tid < D) {
-      for (int j = 0; j < 128 && t0 + j < ctx; ++j) {
-        const int vid = block_id[j / 16];
-        if (vid < 0) continue;
-        const uint8_t c = p.kv[(static_cast<size_t>(vid) * p.n_kv_heads + kvh) * f8_tile_bytes(D) +
-                               (kBlockTokens + j % 16) * D + tid];
-        float v, unused;
-        unpack2<false>(f8_unpack2(c), v, unused);
-        v *= v_scale[j / 16];
-        for (int r = 0; r < p.rows; ++r)  // a row's own causal limit: what it does not see may be NaN
-          if (t0 + j < ctx - p.q_len + r / p.gp + 1) o[r] += w_s[r][j] * v;
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) qb[nr][kk][0] = w[2 * kk], qb[nr][kk][1] = w[2 * kk + 1];
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        c[nr][r] = __shfl_sync(0xffffffffu, cs, (2 * t + r) * 4);
+        hide[nr][r] = p.q_len - 1 - (first_row + 8 * nr + 2 * t + r) / p.group;
+        m[nr][r] = -INFINITY;
+        l[nr][r] = 0.f;
       }
+#pragma unroll
+      for (int i = 0; i < MT; ++i) o[nr][i][0] = o[nr][i][1] = o[nr][i][2] = o[nr][i][3] = 0.f;
     }
   }
-  for (int r = 0; r < p.rows; ++r) {
-    float sum = l[r];
-    for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+
+  // `rem`: context tokens from the tile's first on; `q_len` queries end there.
+  __device__ __forceinline__ void tile(uint32_t base, float ks, float vs, int rem, int q_len, bool residual,
+                                       int lane) {
+    const int g = lane >> 2, t = lane & 3;
+    // Token of row g of the S^T product (and of k-index g of P V), and of row
+    // g + 8: the order in which ldsm_b8_x2_trans hands out V's tokens.
+    const int tok = 4 * (g >> 1) + (g & 1);
+
+    float s[NR][2][4];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) s[nr][i >> 2][i & 3] = 0.f;
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      uint32_t ka[4], kb[4];
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(ka[0]), "=r"(ka[1]), "=r"(ka[2]), "=r"(ka[3])
+                   : "r"(base + f8_chunk_at<D>(tok, D / 64 * t + i)));
+      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(kb[0]), "=r"(kb[1]), "=r"(kb[2]), "=r"(kb[3])
+                   : "r"(base + f8_chunk_at<D>(tok + 2, D / 64 * t + i)));
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t a0 = f8_unpack2(ka[w] & 0xffffu), a1 = f8_unpack2(kb[w] & 0xffffu);
+        const uint32_t a2 = f8_unpack2(ka[w] >> 16), a3 = f8_unpack2(kb[w] >> 16);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)  // two chains of sums
+          mma_16816<false>(s[nr][w & 1], a0, a1, a2, a3, qb[nr][4 * i + w][0], qb[nr][4 * i + w][1]);
+      }
+    }
+
+    // s_V = f 2^e.
+    const uint32_t vbits = __float_as_uint(vs);
+    const int e = static_cast<int>(vbits >> 23) - 127;
+    const float fe = static_cast<float>(e), f = __uint_as_float((vbits & 0x7fffffu) | 0x3f800000u);
+    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+    // Tokens that some row does not see: the context's last q_len - 1, and what is behind it.
+    const bool edge = rem - (q_len - 1) < kBlockTokens;
+    float y[NR][4];
+    bool far = false;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float a = ks * c[nr][i & 1];
+        s[nr][0][i] = (s[nr][0][i] + s[nr][1][i]) * a;
+        y[nr][i] = s[nr][0][i] + (fe - m[nr][i & 1]);
+      }
+      if (edge) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (tok + (i & 2) >= rem - hide[nr][i & 1]) y[nr][i] = s[nr][0][i] = -INFINITY;
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) far = far || y[nr][i] > kF8RefSlack;
+    }
+    if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(s[nr][0][r], s[nr][0][2 + r]) + fe;
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+          if (mx > m[nr][r] + kF8RefSlack) {
+            const float ref = mx - kF8RefBelow;
+            const float alpha = m[nr][r] == -INFINITY ? 0.f : exp2f(m[nr][r] - ref);
+            m[nr][r] = ref;
+            l[nr][r] *= alpha;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[nr][i][r] *= alpha;
+              o[nr][i][2 + r] *= alpha;
+            }
+            y[nr][r] = s[nr][0][r] + (fe - ref);
+            y[nr][2 + r] = s[nr][0][2 + r] + (fe - ref);
+          }
+        }
+    }
+
+    uint32_t ph[NR][2], pl[NR][2];
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) y[nr][i] = ex2_ftz(y[nr][i]);
+      l[nr][0] = fmaf(y[nr][0] + y[nr][2], inv, l[nr][0]);
+      l[nr][1] = fmaf(y[nr][1] + y[nr][3], inv, l[nr][1]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float p0 = y[nr][2 * h] * f, p1 = y[nr][2 * h + 1] * f;
+        const uint32_t hi = pack2<false>(p0, p1);
+        if (residual) {
+          float h0, h1;
+          unpack2<false>(hi, h0, h1);
+          pl[nr][h] = transpose_8x8(pack2<false>(p0 - h0, p1 - h1));
+        }
+        ph[nr][h] = transpose_8x8(hi);
+      }
+    }
+
+    // V bytes of tokens 4 t .. 4 t + 3 behind the context may hold anything: cleared.
+    uint32_t keep = 0xffffffffu;
+    if (rem < kBlockTokens) keep = rem >= 4 * t + 4 ? 0xffffffffu : rem <= 4 * t ? 0u : (1u << (8 * (rem - 4 * t))) - 1u;
+    const uint32_t vbase = base + kBlockTokens * D;
+    const int vt = lane & 15, vc = lane >> 4;
+    if (q_len > 1 && edge && nan_in_edge(vbase, keep, vt, vc)) {
+      edge_with_nan(vbase, rem, q_len, ph, pl, residual, vt, vc, t);
+      return;
+    }
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t r[4];
+      ldsm_b8_x2_trans(vbase + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const uint32_t lo = r[2 * h] & keep, hi = r[2 * h + 1] & keep;
+        const uint32_t a0 = f8_unpack2(lo & 0xffffu), a1 = f8_unpack2(hi & 0xffffu);
+        const uint32_t a2 = f8_unpack2(lo >> 16), a3 = f8_unpack2(hi >> 16);
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+          mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
+          if (residual) mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
+        }
+      }
+    }
+  }
+
+  // Several queries: is there a NaN among the values of the context's last
+  // tokens, which a row that does not see them would take as 0 x NaN?
+  __device__ __noinline__ static bool nan_in_edge(uint32_t vbase, uint32_t keep, int vt, int vc) {
+    uint32_t found = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t r[4];
+      ldsm_b8_x2_trans(vbase + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int h = 0; h < 4; ++h) found |= ((r[h] & keep & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    }
+    return __any_sync(0xffffffffu, found != 0);
+  }
+
+  // The P V step of such a tile, once for each query, over the tokens that it
+  // sees: its rows alone take the result.
+  __device__ __forceinline__ void edge_with_nan(uint32_t vbase, int rem, int q_len, const uint32_t (&ph)[NR][2],
+                                                const uint32_t (&pl)[NR][2], bool residual, int vt, int vc, int t) {
+#pragma unroll 1
+    for (int hq = 0; hq < q_len; ++hq) {  // the queries that do not see the last hq tokens
+      const int n = rem - hq;
+      const uint32_t keep = n >= 4 * t + 4 ? 0xffffffffu : n <= 4 * t ? 0u : (1u << (8 * (n - 4 * t))) - 1u;
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint32_t r[4];
+        ldsm_b8_x2_trans(vbase + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const uint32_t lo = r[2 * h] & keep, hi = r[2 * h + 1] & keep;
+          const uint32_t a0 = f8_unpack2(lo & 0xffffu), a1 = f8_unpack2(hi & 0xffffu);
+          const uint32_t a2 = f8_unpack2(lo >> 16), a3 = f8_unpack2(hi >> 16);
+#pragma unroll
+          for (int nr = 0; nr < NR; ++nr) {
+            float x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) x[k] = o[nr][2 * i + h][k];
+            mma_16816<false>(x, a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
+            if (residual) mma_16816<false>(x, a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              if (hide[nr][k & 1] == hq) o[nr][2 * i + h][k] = x[k];
+          }
+        }
+      }
+    }
+  }
+
+  // The rows' state as a record, or (rec null) their output.
+  __device__ __forceinline__ void finish(const DecodeF8Params& p, float* rec, int b, int kvh, int first_row, int rows,
+                                         int lane) {
+    const int g = lane >> 2, t = lane & 3;
+#pragma unroll
+    for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        float sum = l[nr][r];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = 8 * nr + 2 * t + r;
+        if (row >= rows) continue;
+        if (rec != nullptr) {
+          float* at = rec + row * RS;
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            at[16 * i + g] = o[nr][i][r];
+            at[16 * i + 8 + g] = o[nr][i][2 + r];
+          }
+          if (g == 0) {
+            at[D] = m[nr][r];
+            at[D + 1] = sum;
+          }
+        } else {
+          // A sum of 0 is a row with no token (bad block ids): zeros.  NaN stays NaN.
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          uint16_t* at = p.out + f8_row_at(p, b, kvh, first_row + row, D);
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            const float x = o[nr][i][r] * inv, z = o[nr][i][2 + r] * inv;
+            const uint32_t w = p.bf16 ? pack2<true>(x, z) : pack2<false>(x, z);
+            at[16 * i + g] = static_cast<uint16_t>(w);
+            at[16 * i + 8 + g] = static_cast<uint16_t>(w >> 16);
+          }
+        }
+      }
+  }
+};
+
+// Dims [d0 + DPL lane, + DPL) of one row merged over n pieces, in order:
+//   M = max m_i,  w_i = 2^(m_i - M),  O = sum w_i O_i,  l = sum w_i l_i,
+// online over batches whose loads go out together.  `at(j)`: the row in piece
+// j.  Written to the record row `to`, or normalised to `out`.  kGlobal: the
+// pieces were written by other SMs (read through L2).
+template <int D, int DPL, bool kGlobal, class At>
+__device__ __forceinline__ void f8_merge_row(const At& at, int n, int d0, int lane, bool bf16, float* to,
+                                             uint16_t* out) {
+  constexpr int kBatch = DPL == 1 ? 16 : 8;
+  const int dim = d0 + lane * DPL;
+  float M = -INFINITY, L = 0.f, acc[DPL];
+#pragma unroll
+  for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
+  for (int j0 = 0; j0 < n; j0 += kBatch) {
+    float mj[kBatch], lj[kBatch], o[kBatch][DPL];
+#pragma unroll
+    for (int jj = 0; jj < kBatch; ++jj) {
+      const float* r = at(min(j0 + jj, n - 1));
+      if constexpr (kGlobal) {
+        mj[jj] = ld_cg(r + D);
+        lj[jj] = ld_cg(r + D + 1);
+        if constexpr (DPL == 4) {
+          const float4 v = ld_cg4(r + dim);
+          o[jj][0] = v.x, o[jj][1] = v.y, o[jj][2] = v.z, o[jj][3] = v.w;
+        } else if constexpr (DPL == 2) {
+          const float2 v = ld_cg2(r + dim);
+          o[jj][0] = v.x, o[jj][1] = v.y;
+        } else {
+          o[jj][0] = ld_cg(r + dim);
+        }
+      } else {
+        mj[jj] = r[D];
+        lj[jj] = r[D + 1];
+#pragma unroll
+        for (int i = 0; i < DPL; ++i) o[jj][i] = r[dim + i];
+      }
+    }
+    float Mb = M;
+#pragma unroll
+    for (int jj = 0; jj < kBatch; ++jj)
+      if (j0 + jj < n) Mb = fmaxf(Mb, mj[jj]);
+    // -inf: no token seen so far; those pieces' sums are 0 (or NaN, which stays).
+    const float alpha = M == -INFINITY ? 1.f : exp2f(M - Mb);
+    L *= alpha;
+#pragma unroll
+    for (int i = 0; i < DPL; ++i) acc[i] *= alpha;
+#pragma unroll
+    for (int jj = 0; jj < kBatch; ++jj) {
+      if (j0 + jj >= n) continue;
+      const float w = mj[jj] == -INFINITY ? 1.f : exp2f(mj[jj] - Mb);
+      L = fmaf(w, lj[jj], L);
+#pragma unroll
+      for (int i = 0; i < DPL; ++i) acc[i] = fmaf(w, o[jj][i], acc[i]);
+    }
+    M = Mb;
+  }
+  if (to != nullptr) {
+#pragma unroll
+    for (int i = 0; i < DPL; ++i) to[dim + i] = acc[i];
+    if (lane == 0 && d0 == 0) {
+      to[D] = M;
+      to[D + 1] = L;
+    }
+    return;
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L;
+  uint32_t w[2];
+#pragma unroll
+  for (int i = 0; i < (DPL + 1) / 2; ++i) {
+    const float x = acc[2 * i] * inv, z = DPL > 1 ? acc[(2 * i + 1) % DPL] * inv : 0.f;
+    w[i] = bf16 ? pack2<true>(x, z) : pack2<false>(x, z);
+  }
+  if constexpr (DPL == 4)
+    *reinterpret_cast<uint2*>(out + dim) = make_uint2(w[0], w[1]);
+  else if constexpr (DPL == 2)
+    *reinterpret_cast<uint32_t*>(out + dim) = w[0];
+  else
+    out[dim] = static_cast<uint16_t>(w[0]);
+}
+
+// Rows of a segment that this CTA holds in several units, or shares with other CTAs.
+struct F8Group {
+  int b, hg, st, en;  // the segment's tiles [st, en)
+  int ua, ub;         // first and last unit of this CTA with a piece of it
+};
+
+__host__ __device__ constexpr size_t f8_ring_bytes(int D, int stages) {
+  return static_cast<size_t>(kF8Warps) * stages * f8_tile_bytes(D);
+}
+
+// Shared memory besides the ring: Q of each warp, scales, flags and two barriers of each slot, lengths.
+__host__ __device__ constexpr size_t f8_other_bytes(int D, int NR, int stages, int batch) {
+  return 1024 + static_cast<size_t>(kF8Warps) * 8 * NR * D * 2 + static_cast<size_t>(kF8Warps) * stages * 28 + 16 +
+         (2 * static_cast<size_t>(batch) + 1) * 4;
+}
+
+template <int D, int NR>
+__global__ void __launch_bounds__(kF8Threads, 1)
+    pkv_decode_f8_kernel(const __grid_constant__ CUtensorMap tm, const DecodeF8Params p) {
+  constexpr int kTile = f8_tile_bytes(D);
+  constexpr int kQBytes = 8 * NR * D * 2;
+  constexpr int W = kF8Warps;
+  using Consumer = F8Consumer<D, NR>;
+  constexpr int RS = Consumer::RS;
+
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw);
+  uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int n_slots = W * p.stages;
+  uint8_t* qbufs = ring + static_cast<size_t>(n_slots) * kTile;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(qbufs + W * kQBytes);
+  uint64_t* empty_bar = full_bar + n_slots;
+  float2* slot_scale = reinterpret_cast<float2*>(empty_bar + n_slots);
+  int* slot_bad = reinterpret_cast<int*>(slot_scale + n_slots);
+  volatile int* abort_flag = slot_bad + n_slots;
+  int* prefix = const_cast<int*>(abort_flag) + 4;  // [batch + 1]
+  int* ctxs = prefix + p.batch + 1;                // [batch]
+  __shared__ int warp_sums[W + 1];
+  __shared__ F8Group groups[W + 1];
+  __shared__ int n_groups;
+  __shared__ int last_of[2];  // this CTA finishes: the segment from before it, the one that goes on behind it
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int B = p.batch;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < n_slots; ++i) {
+      mbar_init(&full_bar[i], 2);  // the codes' bytes, and the scales
+      mbar_init(&empty_bar[i], 1);
+    }
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == W && lane == 0) tma_prefetch_desc(&tm);
+
+  // Tiles before each sequence.
+  {
+    const int per = (B + kF8Threads - 1) / kF8Threads;
+    const int lo = min(B, static_cast<int>(threadIdx.x) * per), hi = min(B, lo + per);
+    const int max_ctx = p.max_blocks_per_seq * kBlockTokens;
+    int local = 0;
+    for (int b = lo; b < hi; ++b) {
+      const int c0 = __ldg(p.context_lens + b);
+      int c = clamp_ctx(c0, max_ctx);
+      if (c > 0 && c < p.q_len) c = 0;
+      if (c != c0) flag_error(PKV_DEVERR_CONTEXT);
+      ctxs[b] = c;
+      local += ((c + kBlockTokens - 1) / kBlockTokens) * p.ng;
+    }
+    int incl = local;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int v = __shfl_up_sync(0xffffffffu, incl, off);
+      if (lane >= off) incl += v;
+    }
+    if (lane == 31) warp_sums[warp] = incl;
     __syncthreads();
-    if (lane == 0) red[warp] = sum;
-    __syncthreads();
-    sum = red[0] + red[1] + red[2] + red[3];
-    if (tid < D) {
-      const float y = sum == 0.f ? 0.f : o[r] / sum;
-      p.out[row_at(r) + tid] = static_cast<uint16_t>(p.bf16 ? pack2<true>(y, 0.f) : pack2<false>(y, 0.f));
+    int base = 0;
+    for (int w = 0; w < warp; ++w) base += warp_sums[w];
+    int run = base + incl - local;
+    for (int b = lo; b < hi; ++b) {
+      prefix[b] = run;
+      run += ((ctxs[b] + kBlockTokens - 1) / kBlockTokens) * p.ng;
+    }
+    if (threadIdx.x == kF8Threads - 1) prefix[B] = base + incl;
+  }
+  __syncthreads();
+
+  // Sequences without a token: zeros.
+  for (int b = blockIdx.x; b < B; b += gridDim.x)
+    if (ctxs[b] == 0) {
+      uint4* at = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(b) * p.q_len * p.n_q_heads * D);
+      const int n = p.q_len * p.n_q_heads * (D / 8);
+      for (int i = threadIdx.x; i < n; i += kF8Threads) at[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+
+  const int T = prefix[B];
+  const Sched sc = make_sched(T, min(static_cast<int>(gridDim.x) * W, max(1, T / kF8MinTiles)), 0, 1000);
+  const int u0 = blockIdx.x * W, u_end = min(sc.U, u0 + W);  // this CTA's units
+  if (T == 0 || u0 >= sc.U) return;
+
+  // Rows of segment hg of a sequence: kv head, first of its rows, how many.
+  auto seg_rows = [&](int hg, int& kvh, int& first) {
+    kvh = hg / p.nseg;
+    first = (hg - kvh * p.nseg) * p.rows;
+    return min(p.rows, p.total_rows - first);
+  };
+
+  if (warp == W) {
+    // ---------------- producer: lane w feeds consumer warp w ----------------
+    const uint64_t policy = p.nseg == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+    const int u = u0 + lane;
+    Walk wn;
+    bool walking = false;
+    if (lane < W && u < u_end) walking = walk_begin(wn, prefix, ctxs, B, unit_begin(sc, u), unit_begin(sc, u + 1));
+    struct Ahead {
+      int phys, kvh;
+      bool valid;
+    };
+    // Block ids are read two tiles ahead and used when their tile is issued.
+    auto resolve = [&](Ahead& t) {
+      t.valid = walking;
+      if (!walking) return;
+      t.phys = __ldg(p.block_tables + static_cast<size_t>(wn.b) * p.max_blocks_per_seq + wn.j);
+      t.kvh = wn.hg / p.nseg;
+      walking = wn.k + 1 < wn.k_end;
+      if (walking) walk_next(wn, prefix, ctxs, B, p.ng);
+    };
+    Ahead t0, t1;
+    resolve(t0);
+    resolve(t1);
+    int stage = 0, issued = 0;
+    uint32_t phase = 0;
+    uint64_t idle_since = 0;
+    while (__any_sync(0xffffffffu, t0.valid)) {
+      bool progressed = false;
+      if (t0.valid) {
+        const int slot = lane * p.stages + stage;
+        if (mbar_test_wait(&empty_bar[slot], phase ^ 1u)) {
+          const bool bad = t0.phys < 0 || t0.phys >= p.num_blocks;
+          slot_bad[slot] = bad;  // published by the arrivals below
+          if (bad) {             // nothing is copied; the consumer leaves the tile out
+            flag_error(PKV_DEVERR_BLOCK_ID);
+            mbar_arrive(&full_bar[slot]);
+            mbar_arrive(&full_bar[slot]);
+          } else {
+            const int at = t0.phys * p.n_kv_heads + t0.kvh;
+            mbar_arrive_expect_tx(&full_bar[slot], kTile);
+            tma_load_3d_hint(ring + static_cast<size_t>(slot) * kTile, &tm, &full_bar[slot], at, policy);
+            cp_async_8(&slot_scale[slot], p.scales + at);
+            cp_async_arrive(&full_bar[slot]);
+          }
+          ++issued;
+          if (++stage == p.stages) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          t0 = t1;
+          resolve(t1);
+          progressed = true;
+        }
+      }
+      if (__any_sync(0xffffffffu, progressed)) {
+        idle_since = 0;
+      } else {
+        const uint64_t now = global_timer_ns();
+        if (idle_since == 0) idle_since = now;
+        if (__shfl_sync(0xffffffffu, *abort_flag != 0 || now - idle_since > p.wait_limit_ns, 0)) {
+          if (lane == 0 && *abort_flag == 0) {
+            *abort_flag = 1;
+            flag_error(kDevErrTimeout);
+          }
+          break;
+        }
+      }
+    }
+    // Do not leave while copies of this lane may still be landing.
+    if (lane < W) {
+      for (int s = 0; s < p.stages && s < issued; ++s) {
+        const int cnt = (issued - s + p.stages - 1) / p.stages;
+        const uint64_t since = global_timer_ns();
+        while (!mbar_try_wait(&full_bar[lane * p.stages + s], static_cast<uint32_t>((cnt - 1) & 1))) {
+          if (global_timer_ns() - since > p.wait_limit_ns) {
+            flag_error(kDevErrTimeout);
+            break;
+          }
+        }
+      }
+    }
+  } else if (u0 + warp < u_end) {
+    // ---------------- consumers ----------------
+    const int u = u0 + warp, k0 = unit_begin(sc, u), k1 = unit_begin(sc, u + 1);
+    uint8_t* qbuf = qbufs + warp * kQBytes;
+    auto fetch_q = [&](int b, int hg) {
+      int kvh, first;
+      const int rows = seg_rows(hg, kvh, first);
+      constexpr int kChunks = D / 8;
+      for (int i = lane; i < rows * kChunks; i += 32)
+        cp_async_16(qbuf + i * 16, p.q + f8_row_at(p, b, kvh, first + i / kChunks, D) + (i % kChunks) * 8);
+      cp_async_commit();
+    };
+    Walk wk;
+    walk_begin(wk, prefix, ctxs, B, k0, k1);
+    fetch_q(wk.b, wk.hg);
+    Consumer cs;
+    int stage = 0, kvh = 0, first = 0, rows = 0;
+    uint32_t phase = 0;
+    bool fresh = true;
+    const bool residual = p.bf16 == 0;
+    while (true) {
+      if (fresh) {
+        fresh = false;
+        rows = seg_rows(wk.hg, kvh, first);
+        cp_async_wait_all();
+        __syncwarp();
+        cs.begin(p, qbuf, first, rows, lane);
+        __syncwarp();
+      }
+      const bool last = wk.k + 1 >= k1, seg_last = wk.j == wk.nb - 1;
+      if (seg_last && !last) {  // the next segment's Q
+        Walk nx = wk;
+        walk_next(nx, prefix, ctxs, B, p.ng);
+        fetch_q(nx.b, nx.hg);
+      }
+      const int slot = warp * p.stages + stage;
+      if (!mbar_wait_bounded(&full_bar[slot], phase, abort_flag, p.wait_limit_ns)) break;
+      if (slot_bad[slot] == 0) {
+        const float2 scale = slot_scale[slot];
+        cs.tile(smem_u32(ring + static_cast<size_t>(slot) * kTile), scale.x, scale.y, wk.ctx - wk.j * kBlockTokens,
+                p.q_len, residual, lane);
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&empty_bar[slot]);
+      if (++stage == p.stages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      if (seg_last || last) {
+        // A whole segment's output; a share of one that reaches the unit's
+        // end in this warp's drained ring, else in its record.
+        const int nb = wk.nb, st = wk.k - wk.j;
+        float* rec = nullptr;
+        if (st < k0 || st + nb > k1)
+          rec = last ? reinterpret_cast<float*>(ring + static_cast<size_t>(warp) * p.stages * kTile)
+                     : p.unit_recs + static_cast<size_t>(u) * p.rec_floats;
+        if (last) __syncwarp();
+        cs.finish(p, rec, wk.b, kvh, first, rows, lane);
+        fresh = true;
+      }
+      if (last) break;
+      walk_next(wk, prefix, ctxs, B, p.ng);
+    }
+    cp_async_wait_all();
+  }
+  __syncthreads();
+
+  // ---------------- the CTA's shared segments ----------------
+  // Candidates: the segment that comes from before the CTA, and for each unit
+  // the segment that starts in it and goes on behind it.
+  const int A = unit_begin(sc, u0), E = unit_begin(sc, u_end);
+  if (warp == 0) {
+    bool valid = false;
+    F8Group gr;
+    if (lane <= u_end - u0) {
+      const int u = u0 + max(0, lane - 1);
+      const int k = lane == 0 ? A : unit_begin(sc, u + 1) - 1;
+      Walk w;
+      walk_begin(w, prefix, ctxs, B, k, k + 1);
+      gr.b = w.b;
+      gr.hg = w.hg;
+      gr.st = k - w.j;
+      gr.en = gr.st + w.nb;
+      gr.ua = u;
+      gr.ub = min(unit_of_tile(sc, gr.en - 1), u_end - 1);
+      valid = lane == 0 ? gr.st < A : gr.st >= unit_begin(sc, u) && gr.en > k + 1;
+    }
+    const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+    if (valid) groups[__popc(mask & ((1u << lane) - 1u))] = gr;
+    if (lane == 0) n_groups = __popc(mask);
+  }
+  __syncthreads();
+  const int ng = n_groups;
+  for (int i = warp; i < ng * p.rows; i += W + 1) {
+    const F8Group gr = groups[i / p.rows];
+    const int row = i % p.rows;
+    int kvh, first;
+    if (row >= seg_rows(gr.hg, kvh, first)) continue;
+    auto at = [&](int j) -> const float* {
+      const int u = gr.ua + j;
+      const float* rec = gr.en >= unit_begin(sc, u + 1)
+                             ? reinterpret_cast<const float*>(ring + static_cast<size_t>(u - u0) * p.stages * kTile)
+                             : p.unit_recs + static_cast<size_t>(u) * p.rec_floats;
+      return rec + row * RS;
+    };
+    float* to = nullptr;
+    if (gr.st < A || gr.en > E)
+      to = p.cta_recs + (static_cast<size_t>(blockIdx.x) * 2 + (gr.st < A ? 0 : 1)) * p.rec_floats + row * RS;
+    f8_merge_row<D, D / 32, false>(at, gr.ub - gr.ua + 1, 0, lane, p.bf16 != 0, to,
+                                   p.out + f8_row_at(p, gr.b, kvh, first + row, D));
+  }
+
+  // ---------------- segments shared with other CTAs ----------------
+  // The first group may come from before the CTA, the last may go on behind it (one may do both).
+  const bool from_before = ng > 0 && groups[0].st < A;
+  const bool goes_on = ng > 0 && groups[ng - 1].en > E && groups[ng - 1].st >= A;
+  if (!from_before && !goes_on) return;
+  __threadfence();
+  __syncthreads();
+  if (threadIdx.x < 2) {
+    int fin = 0;
+    if (threadIdx.x == 0 ? from_before : goes_on) {
+      const F8Group& gr = groups[threadIdx.x == 0 ? 0 : ng - 1];
+      const int c0 = unit_of_tile(sc, gr.st) / W, n = unit_of_tile(sc, gr.en - 1) / W - c0 + 1;
+      const unsigned int before = atomicAdd(p.counters + c0, 1u);
+      if (before >= static_cast<unsigned int>(n)) flag_error(PKV_DEVERR_SCHEDULE);
+      if (before + 1 >= static_cast<unsigned int>(n)) {
+        fin = 1;
+        p.counters[c0] = 0;
+      }
+    }
+    last_of[threadIdx.x] = fin;
+    __threadfence();
+  }
+  __syncthreads();
+#pragma unroll 1
+  for (int k = 0; k < 2; ++k) {
+    if (last_of[k] == 0) continue;
+    const F8Group gr = groups[k == 0 ? 0 : ng - 1];
+    const int c0 = unit_of_tile(sc, gr.st) / W, n = unit_of_tile(sc, gr.en - 1) / W - c0 + 1;
+    int kvh, first;
+    const int rows = seg_rows(gr.hg, kvh, first);
+    auto row_at = [&](int row, int j) -> const float* {  // the first CTA's share goes on behind it, the others' come from before
+      return p.cta_recs + (static_cast<size_t>(c0 + j) * 2 + (j == 0 ? 1 : 0)) * p.rec_floats + row * RS;
+    };
+    if (n > 8) {  // many pieces: D / 32 warps share a row
+      for (int i = warp; i < rows * (D / 32); i += W + 1) {
+        const int row = i / (D / 32);
+        f8_merge_row<D, 1, true>([&](int j) { return row_at(row, j); }, n, i % (D / 32) * 32, lane, p.bf16 != 0, nullptr,
+                                 p.out + f8_row_at(p, gr.b, kvh, first + row, D));
+      }
+    } else {
+      for (int row = warp; row < rows; row += W + 1)
+        f8_merge_row<D, D / 32, true>([&](int j) { return row_at(row, j); }, n, 0, lane, p.bf16 != 0, nullptr,
+                                      p.out + f8_row_at(p, gr.b, kvh, first + row, D));
     }
   }
 }
