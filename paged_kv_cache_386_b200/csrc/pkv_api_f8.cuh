@@ -114,13 +114,13 @@ void decode_f8_segments(int total_rows, int* nseg, int* rows) {
 }
 
 size_t decode_f8_workspace(int sm_count, int rows, int head_dim) {
-  const size_t records = static_cast<size_t>(sm_count) * (kF8Warps + 2);  // a unit's each, two of each CTA
+  const size_t records = static_cast<size_t>(sm_count) * (f8_warps(rows <= 8 ? 1 : 2) + 2);  // a unit's each, two of each CTA
   return kF8HeaderBytes + records * rows * (head_dim + 4) * sizeof(float);
 }
 
-template <int D, int NR>
+template <int D, int NR, bool kBf16>
 pkv_status launch_decode_f8(const CUtensorMap& map, DecodeF8Params p, const DeviceInfo& di, cudaStream_t s) {
-  auto kern = pkv_decode_f8_kernel<D, NR>;
+  auto kern = pkv_decode_f8_kernel<D, NR, kBf16>;
   static bool opted_in[kMaxDevices] = {};
   int dev = 0;
   cudaFuncAttributes fa;
@@ -133,11 +133,19 @@ pkv_status launch_decode_f8(const CUtensorMap& map, DecodeF8Params p, const Devi
     opted_in[dev] = true;
   }
   p.stages = kF8MaxStages;
-  auto smem = [&] { return f8_ring_bytes(D, p.stages) + f8_other_bytes(D, NR, p.stages, p.batch); };
+  auto smem = [&] { return f8_smem_bytes(D, f8_warps(NR), p.stages, p.rows, p.batch); };
   while (smem() > static_cast<size_t>(di.smem_optin - kStatic)) --p.stages;
-  if (p.stages < NR + 1) return PKV_ERR_UNSUPPORTED;  // a warp's ring holds a record
-  kern<<<di.sm_count, kF8Threads, smem(), s>>>(map, p);
+  if (p.stages * f8_tile_bytes(D) < p.rec_floats * 4) return PKV_ERR_UNSUPPORTED;  // a warp's ring holds a record
+  kern<<<di.sm_count, f8_warps(NR) * 32, smem(), s>>>(map, p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+template <bool kBf16>
+pkv_status dispatch_decode_f8(int head_dim, const CUtensorMap& map, const DecodeF8Params& p, const DeviceInfo& di,
+                              cudaStream_t s) {
+  if (head_dim == 64)
+    return p.rows <= 8 ? launch_decode_f8<64, 1, kBf16>(map, p, di, s) : launch_decode_f8<64, 2, kBf16>(map, p, di, s);
+  return p.rows <= 8 ? launch_decode_f8<128, 1, kBf16>(map, p, di, s) : launch_decode_f8<128, 2, kBf16>(map, p, di, s);
 }
 
 }  // namespace
@@ -279,7 +287,6 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
   p.ng = n_kv_heads * p.nseg;
   if (static_cast<int64_t>(batch) * max_blocks_per_seq * p.ng > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   p.rec_floats = p.rows * (head_dim + 4);
-  p.bf16 = dtype == PKV_BF16;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = kWaitLimitNs;
 
@@ -302,11 +309,9 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
   }
   p.counters = reinterpret_cast<unsigned int*>(ws);
   p.unit_recs = reinterpret_cast<float*>(ws + kF8HeaderBytes);
-  p.cta_recs = p.unit_recs + static_cast<size_t>(di.sm_count) * kF8Warps * p.rec_floats;
-  if (head_dim == 64)
-    st = p.rows <= 8 ? launch_decode_f8<64, 1>(map, p, di, s) : launch_decode_f8<64, 2>(map, p, di, s);
-  else
-    st = p.rows <= 8 ? launch_decode_f8<128, 1>(map, p, di, s) : launch_decode_f8<128, 2>(map, p, di, s);
+  p.cta_recs = p.unit_recs + static_cast<size_t>(di.sm_count) * f8_warps(p.rows <= 8 ? 1 : 2) * p.rec_floats;
+  st = dtype == PKV_BF16 ? dispatch_decode_f8<true>(head_dim, map, p, di, s)
+                         : dispatch_decode_f8<false>(head_dim, map, p, di, s);
   if (own && cudaFreeAsync(ws, s) != cudaSuccess && st == PKV_OK) st = PKV_ERR_CUDA;
   return st;
 }

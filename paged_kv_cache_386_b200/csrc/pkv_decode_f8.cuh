@@ -4,15 +4,16 @@
 // Work.  A tile is one (block, kv head): K and V codes, 32 D contiguous
 // bytes.  A segment is the context of one sequence for up to 16 rows (query,
 // head) of one kv head.  The tiles of all segments in order are cut into equal
-// ranges, one per consumer warp ("unit"); W consecutive units are a CTA's.
+// ranges, one per warp ("unit"); W consecutive units are a CTA's.  Each warp
+// copies its own tiles, one TMA box each, a ring ahead of their use.
 // Nothing waits for another CTA: a segment that several warps of one CTA
 // share is merged in shared memory when the CTA is done, one that several CTAs
 // share by the CTA that finishes it last (a counter per CTA where such a
 // segment starts), always in the order of the context, so that the bits do
 // not depend on which CTA that is.
 //
-// Arithmetic of a tile (one warp).  With s_K, s_V the block's scales and
-// e = floor(log2 s_V), f = s_V 2^-e:
+// Arithmetic of a warp's step, two tiles (32 tokens) of one segment.  With s_K,
+// s_V a block's scales and e = floor(log2 s_V), f = s_V 2^-e:
 //   S^T = K Q^T            mma m16n8k16 f16: 16 tokens x 8 rows, codes as f16
 //                          (exact), Q as f16 (exact; bf16 rows are first scaled
 //                          by a power of two), fp32 sums
@@ -22,19 +23,13 @@
 // so that a block's V scale costs one addition in the exponent, weights are
 // largest where p V is, and out = O / l.  The reference m is 2^7 below the
 // largest p s_V seen and moves only when a weight would pass 2^14: a vote per
-// tile, a reduction over tokens when it moves (at a segment's first tiles),
+// step, a reduction over tokens when it moves (at a segment's first tiles),
 // and weights keep f16's full precision down to 2^-21 of the largest.  With
 // f16 data the rounding of the weights (2^-12) is as large as that of the
 // output, so their remainders take a second product.
 //
 // Rows on the n side of the product halve the products for 8 rows or fewer
-// (16 f16 MMAs for a tile of 16 x 128 K and V, not 32) and the accumulators.
-//
-// Bound: HBM, 2 D bytes a token and kv head.  A tile of 4 KiB has to be done
-// every 178 cycles of an SM at the measured copy rate; measured, its 64
-// conversions take 49 of them and its MMAs 33 (2.04 each).  Tensor-memory MMAs
-// on the codes would need Q and P cut into e4m3 pieces and a block-wide softmax
-// over 128 tokens, to relieve pipes that are idle most of the time.
+// (16 MMAs for a tile of 16 x 128 K and V, not 32) and the accumulators.
 #pragma once
 
 #include "pkv_append_f8.cuh"
@@ -42,11 +37,10 @@
 
 namespace pkv {
 
-constexpr int kF8Warps = 10;                          // consumer warps (units) of a CTA
-constexpr int kF8Threads = (kF8Warps + 1) * 32;       // and one producer warp
-constexpr int kF8MaxStages = 4;                       // ring slots of a warp
+constexpr int kF8MaxStages = 6;                       // ring slots of a warp
 constexpr int kF8MinTiles = 2;                        // tiles that make a unit worth its merge
 constexpr int kF8HeaderBytes = 4096;                  // workspace: a counter per CTA
+constexpr int kF8BadTile = 0x7fc0bad0;                 // K scale of a tile whose block id is out of range (a NaN)
 constexpr float kF8RefBelow = 7.f, kF8RefSlack = 14.f;
 
 struct DecodeF8Params {
@@ -66,7 +60,6 @@ struct DecodeF8Params {
   int32_t ng;          // segments of a sequence, n_kv * nseg
   int32_t stages;
   int32_t rec_floats;  // rows * (D + 4)
-  int32_t bf16;
   float scale_log2;
   uint64_t wait_limit_ns;
 };
@@ -126,11 +119,40 @@ __device__ __forceinline__ uint32_t f8_chunk_at(int tok, int c) {
   return static_cast<uint32_t>(tok * D + (D == 128 ? c ^ (tok & 7) : c ^ ((tok >> 1) & 3)) * 16);
 }
 
-template <int D, int NR>
+// Token of row g of a tile's S^T product (k-index g of P V), and of row g + 8
+// (4 further); with matrix row i of V at token f8_v_token(i), lane (g, t)'s
+// four V bytes are the tokens of rows 2 t, 2 t + 1, 2 t + 8, 2 t + 9.  Eight
+// successive rows of either are eight rows of the swizzle, so that no read
+// conflicts.
+__device__ __forceinline__ int f8_k_token(int g) { return (g & 3) + 8 * (g >> 2); }
+__device__ __forceinline__ int f8_v_token(int i) { return f8_k_token(2 * (i >> 2) + (i & 1)) + 2 * (i & 2); }
+
+// Four codes to two packed half pairs (exact).
+__device__ __forceinline__ void f8_unpack4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %2;\n cvt.rn.f16x2.e4m3x2 %0, l;\n cvt.rn.f16x2.e4m3x2 %1, h;\n}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(w));
+}
+
+__device__ __forceinline__ void lds128(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+
+// A step's tiles: shared-memory address and scales; a dead one (behind the
+// segment or the unit, or of a bad block id) adds nothing.
+struct F8Step {
+  uint32_t base[2];
+  float ks[2], vs[2];
+  bool dead[2];
+  int rem;  // context tokens from the first tile's first on
+};
+
+template <int D, int NR, bool kBf16>
 struct F8Consumer {
-  static constexpr int KS = D / 16;    // k-steps of S
-  static constexpr int MT = D / 16;    // 16-dim tiles of O
-  static constexpr int RS = D + 4;     // floats of a record's row: O, m, l, and padding against bank conflicts
+  static constexpr bool kRest = !kBf16;  // P's rounding to f16 is followed by its remainder
+  static constexpr int KS = D / 16;      // k-steps of S
+  static constexpr int MT = D / 16;      // 16-dim tiles of O
+  static constexpr int RS = D + 4;       // floats of a record's row: O, m, l, and padding against bank conflicts
   uint32_t qb[NR][KS][2];
   float o[NR][MT][4];                  // dims 16 mt + g (+ 8), rows 8 nr + 2 t (+ 1)
   float m[NR][2], l[NR][2], c[NR][2];  // reference, sum over this lane's tokens, factor of s_K, of those rows
@@ -151,7 +173,7 @@ struct F8Consumer {
         w[4 * i] = v.x, w[4 * i + 1] = v.y, w[4 * i + 2] = v.z, w[4 * i + 3] = v.w;
       }
       float cs = p.scale_log2;
-      if (p.bf16) {
+      if constexpr (kBf16) {
         // The row's largest magnitude to [2^13, 2^14): what is more than 2^28
         // times smaller keeps fewer bits.
         float mx = 0.f;
@@ -167,14 +189,13 @@ struct F8Consumer {
         // 2^(13 - e) as two factors that are both in range.
         const int up = 13 - e, u1 = up / 2, u2 = up - u1;
         const float f1 = __uint_as_float((u1 + 127) << 23), f2 = __uint_as_float((u2 + 127) << 23);
-        const float d1 = __uint_as_float((127 - u1) << 23), d2 = __uint_as_float((127 - u2) << 23);
 #pragma unroll
         for (int i = 0; i < DL / 2; ++i) {
           float lo, hi;
           unpack2<true>(w[i], lo, hi);
           w[i] = pack2<false>(lo * f1 * f2, hi * f1 * f2);
         }
-        cs = p.scale_log2 * d1 * d2;
+        cs = p.scale_log2 * __uint_as_float((127 - u1) << 23) * __uint_as_float((127 - u2) << 23);
       }
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) qb[nr][kk][0] = w[2 * kk], qb[nr][kk][1] = w[2 * kk + 1];
@@ -190,69 +211,78 @@ struct F8Consumer {
     }
   }
 
-  // `rem`: context tokens from the tile's first on; `q_len` queries end there.
-  __device__ __forceinline__ void tile(uint32_t base, float ks, float vs, int rem, int q_len, bool residual,
-                                       int lane) {
+  __device__ __forceinline__ void step(const F8Step& st, int q_len, int lane) {
     const int g = lane >> 2, t = lane & 3;
-    // Token of row g of the S^T product (and of k-index g of P V), and of row
-    // g + 8: the order in which ldsm_b8_x2_trans hands out V's tokens.
-    const int tok = 4 * (g >> 1) + (g & 1);
+    const int tok = f8_k_token(g);
 
-    float s[NR][2][4];
+    float s[2][NR][4], y[2][NR][4], a[2][NR][2], fe[2], f[2], inv[2];
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr)
+    for (int h = 0; h < 2; ++h) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) s[nr][i >> 2][i & 3] = 0.f;
+      for (int i = 0; i < NR * 4; ++i) s[h][i >> 2][i & 3] = 0.f;
 #pragma unroll
-    for (int i = 0; i < D / 64; ++i) {
-      uint32_t ka[4], kb[4];
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(ka[0]), "=r"(ka[1]), "=r"(ka[2]), "=r"(ka[3])
-                   : "r"(base + f8_chunk_at<D>(tok, D / 64 * t + i)));
-      asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                   : "=r"(kb[0]), "=r"(kb[1]), "=r"(kb[2]), "=r"(kb[3])
-                   : "r"(base + f8_chunk_at<D>(tok + 2, D / 64 * t + i)));
+      for (int i = 0; i < D / 64; ++i) {
+        uint32_t ka[4], kb[4];
+        lds128(st.base[h] + f8_chunk_at<D>(tok, D / 64 * t + i), ka);
+        lds128(st.base[h] + f8_chunk_at<D>(tok + 4, D / 64 * t + i), kb);
 #pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const uint32_t a0 = f8_unpack2(ka[w] & 0xffffu), a1 = f8_unpack2(kb[w] & 0xffffu);
-        const uint32_t a2 = f8_unpack2(ka[w] >> 16), a3 = f8_unpack2(kb[w] >> 16);
+        for (int w = 0; w < 4; ++w) {
+          uint32_t a0, a1, a2, a3;
+          f8_unpack4(ka[w], a0, a2);
+          f8_unpack4(kb[w], a1, a3);
 #pragma unroll
-        for (int nr = 0; nr < NR; ++nr)  // two chains of sums
-          mma_16816<false>(s[nr][w & 1], a0, a1, a2, a3, qb[nr][4 * i + w][0], qb[nr][4 * i + w][1]);
+          for (int nr = 0; nr < NR; ++nr)
+            mma_16816<false>(s[h][nr], a0, a1, a2, a3, qb[nr][4 * i + w][0], qb[nr][4 * i + w][1]);
+        }
+      }
+      // s_V = f 2^e.
+      const uint32_t vbits = __float_as_uint(st.vs[h]);
+      const int e = static_cast<int>(vbits >> 23) - 127;
+      fe[h] = static_cast<float>(e);
+      f[h] = __uint_as_float((vbits & 0x7fffffu) | 0x3f800000u);
+      inv[h] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr) {
+        a[h][nr][0] = st.ks[h] * c[nr][0];
+        a[h][nr][1] = st.ks[h] * c[nr][1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) y[h][nr][i] = fmaf(s[h][nr][i], a[h][nr][i & 1], fe[h] - m[nr][i & 1]);
       }
     }
-
-    // s_V = f 2^e.
-    const uint32_t vbits = __float_as_uint(vs);
-    const int e = static_cast<int>(vbits >> 23) - 127;
-    const float fe = static_cast<float>(e), f = __uint_as_float((vbits & 0x7fffffu) | 0x3f800000u);
-    const float inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-    // Tokens that some row does not see: the context's last q_len - 1, and what is behind it.
-    const bool edge = rem - (q_len - 1) < kBlockTokens;
-    float y[NR][4];
+    // Tokens that some row does not see: the context's last q_len - 1, and dead tiles.
+    const bool edge = st.dead[0] || st.dead[1] || st.rem - (q_len - 1) < 2 * kBlockTokens;
+    auto hidden = [&](int h, int nr, int i) {
+      return st.dead[h] || 16 * h + tok + 2 * (i & 2) >= st.rem - hide[nr][i & 1];
+    };
+    if (edge) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (hidden(h, nr, i)) y[h][nr][i] = s[h][nr][i] = -INFINITY;
+    }
     bool far = false;
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float a = ks * c[nr][i & 1];
-        s[nr][0][i] = (s[nr][0][i] + s[nr][1][i]) * a;
-        y[nr][i] = s[nr][0][i] + (fe - m[nr][i & 1]);
-      }
-      if (edge) {
+      for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (tok + (i & 2) >= rem - hide[nr][i & 1]) y[nr][i] = s[nr][0][i] = -INFINITY;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) far = far || y[nr][i] > kF8RefSlack;
-    }
+        for (int i = 0; i < 4; ++i) far = far || y[h][nr][i] > kF8RefSlack;
     if (__any_sync(0xffffffffu, far)) {
+      // Where a row's largest grew by more than the slack: a new reference.
+      // (A hidden score is -inf; times a negative factor it would not be.)
 #pragma unroll
       for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          float mx = fmaxf(s[nr][0][r], s[nr][0][2 + r]) + fe;
+          float mx = -INFINITY;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = r; i < 4; i += 2)
+              if (s[h][nr][i] != -INFINITY) mx = fmaxf(mx, fmaf(s[h][nr][i], a[h][nr][r], fe[h]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -266,104 +296,117 @@ struct F8Consumer {
               o[nr][i][r] *= alpha;
               o[nr][i][2 + r] *= alpha;
             }
-            y[nr][r] = s[nr][0][r] + (fe - ref);
-            y[nr][2 + r] = s[nr][0][2 + r] + (fe - ref);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int i = r; i < 4; i += 2)
+                y[h][nr][i] = s[h][nr][i] == -INFINITY ? -INFINITY : fmaf(s[h][nr][i], a[h][nr][r], fe[h] - ref);
           }
         }
     }
 
-    uint32_t ph[NR][2], pl[NR][2];
+    uint32_t ph[2][NR][2], pl[2][NR][2];  // the weights as b operands, and their remainders
 #pragma unroll
-    for (int nr = 0; nr < NR; ++nr) {
+    for (int h = 0; h < 2; ++h)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) y[nr][i] = ex2_ftz(y[nr][i]);
-      l[nr][0] = fmaf(y[nr][0] + y[nr][2], inv, l[nr][0]);
-      l[nr][1] = fmaf(y[nr][1] + y[nr][3], inv, l[nr][1]);
+      for (int nr = 0; nr < NR; ++nr) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float p0 = y[nr][2 * h] * f, p1 = y[nr][2 * h + 1] * f;
-        const uint32_t hi = pack2<false>(p0, p1);
-        if (residual) {
-          float h0, h1;
-          unpack2<false>(hi, h0, h1);
-          pl[nr][h] = transpose_8x8(pack2<false>(p0 - h0, p1 - h1));
+        for (int i = 0; i < 4; ++i) y[h][nr][i] = ex2_ftz(y[h][nr][i]);
+        l[nr][0] = fmaf(y[h][nr][0] + y[h][nr][2], inv[h], l[nr][0]);
+        l[nr][1] = fmaf(y[h][nr][1] + y[h][nr][3], inv[h], l[nr][1]);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float p0 = y[h][nr][2 * k] * f[h], p1 = y[h][nr][2 * k + 1] * f[h];
+          const uint32_t hi = pack2<false>(p0, p1);
+          ph[h][nr][k] = transpose_8x8(hi);
+          if constexpr (kRest) {
+            float h0, h1;
+            unpack2<false>(hi, h0, h1);
+            pl[h][nr][k] = transpose_8x8(pack2<false>(p0 - h0, p1 - h1));
+          }
         }
-        ph[nr][h] = transpose_8x8(hi);
+      }
+
+    const uint32_t v0 = st.base[0] + kBlockTokens * D, v1 = st.base[1] + kBlockTokens * D;
+    if (!edge) {
+      pv<false>(v0, 0u, ph[0], pl[0], lane);
+      pv<false>(v1, 0u, ph[1], pl[1], lane);
+    } else {
+      // V bytes behind the context may hold anything: cleared.
+      const int n0 = st.dead[0] ? 0 : st.rem, n1 = st.dead[1] ? 0 : st.rem - kBlockTokens;
+      if (q_len > 1 && (nan_in(v0, keep_bytes(n0, t), lane) || nan_in(v1, keep_bytes(n1, t), lane))) {
+        // A row that does not see a NaN's token would take 0 x NaN: the
+        // product once for each query, over the tokens that it sees.
+#pragma unroll 1
+        for (int hq = 0; hq < q_len; ++hq) {
+          pv<true>(v0, keep_bytes(n0 - hq, t), ph[0], pl[0], lane, hq);
+          pv<true>(v1, keep_bytes(n1 - hq, t), ph[1], pl[1], lane, hq);
+        }
+      } else {
+        pv<true>(v0, keep_bytes(n0, t), ph[0], pl[0], lane);
+        pv<true>(v1, keep_bytes(n1, t), ph[1], pl[1], lane);
       }
     }
+  }
 
-    // V bytes of tokens 4 t .. 4 t + 3 behind the context may hold anything: cleared.
-    uint32_t keep = 0xffffffffu;
-    if (rem < kBlockTokens) keep = rem >= 4 * t + 4 ? 0xffffffffu : rem <= 4 * t ? 0u : (1u << (8 * (rem - 4 * t))) - 1u;
-    const uint32_t vbase = base + kBlockTokens * D;
-    const int vt = lane & 15, vc = lane >> 4;
-    if (q_len > 1 && edge && nan_in_edge(vbase, keep, vt, vc)) {
-      edge_with_nan(vbase, rem, q_len, ph, pl, residual, vt, vc, t);
-      return;
-    }
+  // Mask of this lane's four V bytes, of a tile with n tokens.
+  __device__ __forceinline__ static uint32_t keep_bytes(int n, int t) {
+    uint32_t keep = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (f8_v_token(4 * t + i) < n) keep |= 0xffu << (8 * i);
+    return keep;
+  }
+
+  // O^T += V^T P^T of one tile; only_hide >= 0: only rows with that many hidden tokens take it.
+  template <bool kKeep>
+  __device__ __forceinline__ void pv(uint32_t v, uint32_t keep, const uint32_t (&ph)[NR][2], const uint32_t (&pl)[NR][2],
+                                     int lane, int only_hide = -1) {
+    const int vt = f8_v_token(lane & 15), vc = lane >> 4;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t r[4];
-      ldsm_b8_x2_trans(vbase + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
+      ldsm_b8_x2_trans(v + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
+      if constexpr (kKeep) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) r[k] &= keep;
+      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        const uint32_t lo = r[2 * h] & keep, hi = r[2 * h + 1] & keep;
-        const uint32_t a0 = f8_unpack2(lo & 0xffffu), a1 = f8_unpack2(hi & 0xffffu);
-        const uint32_t a2 = f8_unpack2(lo >> 16), a3 = f8_unpack2(hi >> 16);
+        uint32_t a0, a1, a2, a3;
+        f8_unpack4(r[2 * h], a0, a2);
+        f8_unpack4(r[2 * h + 1], a1, a3);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-          mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
-          if (residual) mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
-        }
-      }
-    }
-  }
-
-  // Several queries: is there a NaN among the values of the context's last
-  // tokens, which a row that does not see them would take as 0 x NaN?
-  __device__ __noinline__ static bool nan_in_edge(uint32_t vbase, uint32_t keep, int vt, int vc) {
-    uint32_t found = 0;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint32_t r[4];
-      ldsm_b8_x2_trans(vbase + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
-#pragma unroll
-      for (int h = 0; h < 4; ++h) found |= ((r[h] & keep & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    }
-    return __any_sync(0xffffffffu, found != 0);
-  }
-
-  // The P V step of such a tile, once for each query, over the tokens that it
-  // sees: its rows alone take the result.
-  __device__ __forceinline__ void edge_with_nan(uint32_t vbase, int rem, int q_len, const uint32_t (&ph)[NR][2],
-                                                const uint32_t (&pl)[NR][2], bool residual, int vt, int vc, int t) {
-#pragma unroll 1
-    for (int hq = 0; hq < q_len; ++hq) {  // the queries that do not see the last hq tokens
-      const int n = rem - hq;
-      const uint32_t keep = n >= 4 * t + 4 ? 0xffffffffu : n <= 4 * t ? 0u : (1u << (8 * (n - 4 * t))) - 1u;
-#pragma unroll
-      for (int i = 0; i < D / 32; ++i) {
-        uint32_t r[4];
-        ldsm_b8_x2_trans(vbase + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const uint32_t lo = r[2 * h] & keep, hi = r[2 * h + 1] & keep;
-          const uint32_t a0 = f8_unpack2(lo & 0xffffu), a1 = f8_unpack2(hi & 0xffffu);
-          const uint32_t a2 = f8_unpack2(lo >> 16), a3 = f8_unpack2(hi >> 16);
-#pragma unroll
-          for (int nr = 0; nr < NR; ++nr) {
+          if constexpr (kKeep) {
             float x[4];
 #pragma unroll
             for (int k = 0; k < 4; ++k) x[k] = o[nr][2 * i + h][k];
             mma_16816<false>(x, a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
-            if (residual) mma_16816<false>(x, a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
+            if constexpr (kRest) mma_16816<false>(x, a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              if (hide[nr][k & 1] == hq) o[nr][2 * i + h][k] = x[k];
+              if (only_hide < 0 || hide[nr][k & 1] == only_hide) o[nr][2 * i + h][k] = x[k];
+          } else {
+            mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
+            if constexpr (kRest) mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
           }
         }
       }
     }
+  }
+
+  __device__ __forceinline__ static bool nan_in(uint32_t v, uint32_t keep, int lane) {
+    const int vt = f8_v_token(lane & 15), vc = lane >> 4;
+    uint32_t found = 0;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      uint32_t r[4];
+      ldsm_b8_x2_trans(v + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) found |= ((r[k] & keep & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+    }
+    return __any_sync(0xffffffffu, found != 0);
   }
 
   // The rows' state as a record, or (rec null) their output.
@@ -398,7 +441,7 @@ struct F8Consumer {
 #pragma unroll
           for (int i = 0; i < MT; ++i) {
             const float x = o[nr][i][r] * inv, z = o[nr][i][2 + r] * inv;
-            const uint32_t w = p.bf16 ? pack2<true>(x, z) : pack2<false>(x, z);
+            const uint32_t w = pack2<kBf16>(x, z);
             at[16 * i + g] = static_cast<uint16_t>(w);
             at[16 * i + 8 + g] = static_cast<uint16_t>(w >> 16);
           }
@@ -412,9 +455,8 @@ struct F8Consumer {
 // online over batches whose loads go out together.  `at(j)`: the row in piece
 // j.  Written to the record row `to`, or normalised to `out`.  kGlobal: the
 // pieces were written by other SMs (read through L2).
-template <int D, int DPL, bool kGlobal, class At>
-__device__ __forceinline__ void f8_merge_row(const At& at, int n, int d0, int lane, bool bf16, float* to,
-                                             uint16_t* out) {
+template <int D, int DPL, bool kGlobal, bool kBf16, class At>
+__device__ __forceinline__ void f8_merge_row(const At& at, int n, int d0, int lane, float* to, uint16_t* out) {
   constexpr int kBatch = DPL == 1 ? 16 : 8;
   const int dim = d0 + lane * DPL;
   float M = -INFINITY, L = 0.f, acc[DPL];
@@ -477,7 +519,7 @@ __device__ __forceinline__ void f8_merge_row(const At& at, int n, int d0, int la
 #pragma unroll
   for (int i = 0; i < (DPL + 1) / 2; ++i) {
     const float x = acc[2 * i] * inv, z = DPL > 1 ? acc[(2 * i + 1) % DPL] * inv : 0.f;
-    w[i] = bf16 ? pack2<true>(x, z) : pack2<false>(x, z);
+    w[i] = pack2<kBf16>(x, z);
   }
   if constexpr (DPL == 4)
     *reinterpret_cast<uint2*>(out + dim) = make_uint2(w[0], w[1]);
@@ -493,58 +535,56 @@ struct F8Group {
   int ua, ub;         // first and last unit of this CTA with a piece of it
 };
 
-__host__ __device__ constexpr size_t f8_ring_bytes(int D, int stages) {
-  return static_cast<size_t>(kF8Warps) * stages * f8_tile_bytes(D);
-}
+// Warps of a CTA, each a unit.
+__host__ __device__ constexpr int f8_warps(int NR) { return NR == 1 ? 12 : 8; }
 
-// Shared memory besides the ring: Q of each warp, scales, flags and two barriers of each slot, lengths.
-__host__ __device__ constexpr size_t f8_other_bytes(int D, int NR, int stages, int batch) {
-  return 1024 + static_cast<size_t>(kF8Warps) * 8 * NR * D * 2 + static_cast<size_t>(kF8Warps) * stages * 28 + 16 +
+// Shared memory: each warp's ring, its Q rows, a scale pair and a barrier of each slot; lengths.
+__host__ __device__ constexpr size_t f8_smem_bytes(int D, int W, int stages, int rows, int batch) {
+  return 1024 + static_cast<size_t>(W) * (stages * (f8_tile_bytes(D) + 16) + rows * D * 2) + 16 +
          (2 * static_cast<size_t>(batch) + 1) * 4;
 }
 
-template <int D, int NR>
-__global__ void __launch_bounds__(kF8Threads, 1)
+template <int D, int NR, bool kBf16>
+__global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     pkv_decode_f8_kernel(const __grid_constant__ CUtensorMap tm, const DecodeF8Params p) {
   constexpr int kTile = f8_tile_bytes(D);
-  constexpr int kQBytes = 8 * NR * D * 2;
-  constexpr int W = kF8Warps;
-  using Consumer = F8Consumer<D, NR>;
+  constexpr int W = f8_warps(NR), kThreads = W * 32;
+  using Consumer = F8Consumer<D, NR, kBf16>;
   constexpr int RS = Consumer::RS;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
-  uint8_t* ring = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  const int n_slots = W * p.stages;
-  uint8_t* qbufs = ring + static_cast<size_t>(n_slots) * kTile;
-  uint64_t* full_bar = reinterpret_cast<uint64_t*>(qbufs + W * kQBytes);
-  uint64_t* empty_bar = full_bar + n_slots;
-  float2* slot_scale = reinterpret_cast<float2*>(empty_bar + n_slots);
-  int* slot_bad = reinterpret_cast<int*>(slot_scale + n_slots);
-  volatile int* abort_flag = slot_bad + n_slots;
+  uint8_t* rings = smem_raw + (((raw + 1023u) & ~1023u) - raw);
+  const int S = p.stages, q_bytes = p.rows * D * 2;
+  uint8_t* qbufs = rings + static_cast<size_t>(W) * S * kTile;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(qbufs + W * q_bytes);  // [W][S]: the slot's copies have landed
+  float2* slot_scales = reinterpret_cast<float2*>(bars + W * S);      // [W][S]
+  volatile int* abort_flag = reinterpret_cast<int*>(slot_scales + W * S);
   int* prefix = const_cast<int*>(abort_flag) + 4;  // [batch + 1]
   int* ctxs = prefix + p.batch + 1;                // [batch]
-  __shared__ int warp_sums[W + 1];
+  __shared__ int warp_sums[W];
   __shared__ F8Group groups[W + 1];
   __shared__ int n_groups;
   __shared__ int last_of[2];  // this CTA finishes: the segment from before it, the one that goes on behind it
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int B = p.batch;
+  uint8_t* ring = rings + static_cast<size_t>(warp) * S * kTile;  // this warp's
+  uint64_t* bar = bars + warp * S;
+  float2* slot_scale = slot_scales + warp * S;
 
   if (threadIdx.x == 0) {
-    for (int i = 0; i < n_slots; ++i) {
-      mbar_init(&full_bar[i], 2);  // the codes' bytes, and the scales
-      mbar_init(&empty_bar[i], 1);
-    }
+    tma_prefetch_desc(&tm);
     *abort_flag = 0;
+  }
+  if (lane == 0) {
+    for (int i = 0; i < S; ++i) mbar_init(&bar[i], 2);  // the codes' bytes, and the scales
     mbar_fence_init();
   }
-  if (warp == W && lane == 0) tma_prefetch_desc(&tm);
 
   // Tiles before each sequence.
   {
-    const int per = (B + kF8Threads - 1) / kF8Threads;
+    const int per = (B + kThreads - 1) / kThreads;
     const int lo = min(B, static_cast<int>(threadIdx.x) * per), hi = min(B, lo + per);
     const int max_ctx = p.max_blocks_per_seq * kBlockTokens;
     int local = 0;
@@ -571,7 +611,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       prefix[b] = run;
       run += ((ctxs[b] + kBlockTokens - 1) / kBlockTokens) * p.ng;
     }
-    if (threadIdx.x == kF8Threads - 1) prefix[B] = base + incl;
+    if (threadIdx.x == kThreads - 1) prefix[B] = base + incl;
   }
   __syncthreads();
 
@@ -580,7 +620,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     if (ctxs[b] == 0) {
       uint4* at = reinterpret_cast<uint4*>(p.out + static_cast<size_t>(b) * p.q_len * p.n_q_heads * D);
       const int n = p.q_len * p.n_q_heads * (D / 8);
-      for (int i = threadIdx.x; i < n; i += kF8Threads) at[i] = make_uint4(0u, 0u, 0u, 0u);
+      for (int i = threadIdx.x; i < n; i += kThreads) at[i] = make_uint4(0u, 0u, 0u, 0u);
     }
 
   const int T = prefix[B];
@@ -595,91 +635,61 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     return min(p.rows, p.total_rows - first);
   };
 
-  if (warp == W) {
-    // ---------------- producer: lane w feeds consumer warp w ----------------
-    const uint64_t policy = p.nseg == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
-    const int u = u0 + lane;
-    Walk wn;
-    bool walking = false;
-    if (lane < W && u < u_end) walking = walk_begin(wn, prefix, ctxs, B, unit_begin(sc, u), unit_begin(sc, u + 1));
-    struct Ahead {
-      int phys, kvh;
-      bool valid;
-    };
-    // Block ids are read two tiles ahead and used when their tile is issued.
-    auto resolve = [&](Ahead& t) {
-      t.valid = walking;
-      if (!walking) return;
-      t.phys = __ldg(p.block_tables + static_cast<size_t>(wn.b) * p.max_blocks_per_seq + wn.j);
-      t.kvh = wn.hg / p.nseg;
-      walking = wn.k + 1 < wn.k_end;
-      if (walking) walk_next(wn, prefix, ctxs, B, p.ng);
-    };
-    Ahead t0, t1;
-    resolve(t0);
-    resolve(t1);
-    int stage = 0, issued = 0;
-    uint32_t phase = 0;
-    uint64_t idle_since = 0;
-    while (__any_sync(0xffffffffu, t0.valid)) {
-      bool progressed = false;
-      if (t0.valid) {
-        const int slot = lane * p.stages + stage;
-        if (mbar_test_wait(&empty_bar[slot], phase ^ 1u)) {
-          const bool bad = t0.phys < 0 || t0.phys >= p.num_blocks;
-          slot_bad[slot] = bad;  // published by the arrivals below
-          if (bad) {             // nothing is copied; the consumer leaves the tile out
-            flag_error(PKV_DEVERR_BLOCK_ID);
-            mbar_arrive(&full_bar[slot]);
-            mbar_arrive(&full_bar[slot]);
-          } else {
-            const int at = t0.phys * p.n_kv_heads + t0.kvh;
-            mbar_arrive_expect_tx(&full_bar[slot], kTile);
-            tma_load_3d_hint(ring + static_cast<size_t>(slot) * kTile, &tm, &full_bar[slot], at, policy);
-            cp_async_8(&slot_scale[slot], p.scales + at);
-            cp_async_arrive(&full_bar[slot]);
-          }
-          ++issued;
-          if (++stage == p.stages) {
-            stage = 0;
-            phase ^= 1u;
-          }
-          t0 = t1;
-          resolve(t1);
-          progressed = true;
-        }
-      }
-      if (__any_sync(0xffffffffu, progressed)) {
-        idle_since = 0;
-      } else {
-        const uint64_t now = global_timer_ns();
-        if (idle_since == 0) idle_since = now;
-        if (__shfl_sync(0xffffffffu, *abort_flag != 0 || now - idle_since > p.wait_limit_ns, 0)) {
-          if (lane == 0 && *abort_flag == 0) {
-            *abort_flag = 1;
-            flag_error(kDevErrTimeout);
-          }
-          break;
-        }
-      }
-    }
-    // Do not leave while copies of this lane may still be landing.
-    if (lane < W) {
-      for (int s = 0; s < p.stages && s < issued; ++s) {
-        const int cnt = (issued - s + p.stages - 1) / p.stages;
-        const uint64_t since = global_timer_ns();
-        while (!mbar_try_wait(&full_bar[lane * p.stages + s], static_cast<uint32_t>((cnt - 1) & 1))) {
-          if (global_timer_ns() - since > p.wait_limit_ns) {
-            flag_error(kDevErrTimeout);
-            break;
-          }
-        }
-      }
-    }
-  } else if (u0 + warp < u_end) {
-    // ---------------- consumers ----------------
+  if (u0 + warp < u_end) {
     const int u = u0 + warp, k0 = unit_begin(sc, u), k1 = unit_begin(sc, u + 1);
-    uint8_t* qbuf = qbufs + warp * kQBytes;
+    const uint64_t policy = p.nseg == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
+
+    // Issue side: the warp copies its own tiles, S ahead of their use.  Block
+    // ids come in windows of 32 (lane i holds entry wj + i of sequence wb's
+    // table); the window that is needed next is loaded when one is taken.
+    Walk wi;
+    walk_begin(wi, prefix, ctxs, B, k0, k1);
+    auto table = [&](int b, int j) {
+      const int at = j + lane;
+      return at < p.max_blocks_per_seq ? __ldg(p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq + at) : -1;
+    };
+    int wb = -1, wj = 0, ids = 0, nxb = -1, nxj = 0, nx_ids = 0;
+    auto window = [&]() {
+      if (wi.b == wb && wi.j >= wj && wi.j < wj + 32) return;
+      if (wi.b == nxb && wi.j >= nxj && wi.j < nxj + 32) {
+        wb = nxb, wj = nxj, ids = nx_ids;
+      } else {
+        wb = wi.b, wj = wi.nb <= 32 ? 0 : wi.j;
+        ids = table(wb, wj);
+      }
+      nxb = wb, nxj = 0;
+      if (wj + 32 < wi.nb) {
+        nxj = wj + 32;
+      } else if (wi.hg + 1 == p.ng || wi.nb <= 32) {  // else the next head of the same sequence, from its start
+        do {
+          ++nxb;
+        } while (nxb < B && ctxs[nxb] == 0);
+      }
+      if (nxb < B) nx_ids = table(nxb, nxj);
+    };
+    auto issue = [&](int slot) {
+      window();
+      const int phys = __shfl_sync(0xffffffffu, ids, wi.j - wj);
+      if (lane == 0) {
+        if (phys < 0 || phys >= p.num_blocks) {  // nothing is copied; a NaN K scale marks the tile
+          flag_error(PKV_DEVERR_BLOCK_ID);
+          slot_scale[slot] = make_float2(__int_as_float(kF8BadTile), 0.f);
+          mbar_arrive(&bar[slot]);
+          mbar_arrive(&bar[slot]);
+        } else {
+          const int at = phys * p.n_kv_heads + wi.hg / p.nseg;
+          mbar_arrive_expect_tx(&bar[slot], kTile);
+          tma_load_3d_hint(ring + slot * kTile, &tm, &bar[slot], at, policy);
+          cp_async_8(&slot_scale[slot], p.scales + at);
+          cp_async_arrive(&bar[slot]);
+        }
+      }
+      walk_next(wi, prefix, ctxs, B, p.ng);
+    };
+    int issued = 0;
+    for (; issued < S && wi.k < k1; ++issued) issue(issued);
+
+    uint8_t* qbuf = qbufs + warp * q_bytes;
     auto fetch_q = [&](int b, int hg) {
       int kvh, first;
       const int rows = seg_rows(hg, kvh, first);
@@ -692,10 +702,9 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     walk_begin(wk, prefix, ctxs, B, k0, k1);
     fetch_q(wk.b, wk.hg);
     Consumer cs;
-    int stage = 0, kvh = 0, first = 0, rows = 0;
+    int slot = 0, kvh = 0, first = 0, rows = 0;
     uint32_t phase = 0;
-    bool fresh = true;
-    const bool residual = p.bf16 == 0;
+    bool fresh = true, ok = true;
     while (true) {
       if (fresh) {
         fresh = false;
@@ -705,41 +714,64 @@ __global__ void __launch_bounds__(kF8Threads, 1)
         cs.begin(p, qbuf, first, rows, lane);
         __syncwarp();
       }
-      const bool last = wk.k + 1 >= k1, seg_last = wk.j == wk.nb - 1;
+      const int n = min(min(2, wk.nb - wk.j), k1 - wk.k);  // tiles of this step
+      const bool last = wk.k + n >= k1, seg_last = wk.j + n >= wk.nb;
       if (seg_last && !last) {  // the next segment's Q
         Walk nx = wk;
+        nx.j = nx.nb - 1;
         walk_next(nx, prefix, ctxs, B, p.ng);
         fetch_q(nx.b, nx.hg);
       }
-      const int slot = warp * p.stages + stage;
-      if (!mbar_wait_bounded(&full_bar[slot], phase, abort_flag, p.wait_limit_ns)) break;
-      if (slot_bad[slot] == 0) {
-        const float2 scale = slot_scale[slot];
-        cs.tile(smem_u32(ring + static_cast<size_t>(slot) * kTile), scale.x, scale.y, wk.ctx - wk.j * kBlockTokens,
-                p.q_len, residual, lane);
+      const int slot1 = slot + 1 == S ? 0 : slot + 1;
+      const uint32_t phase1 = phase ^ (slot1 == 0 ? 1u : 0u);
+      ok = mbar_wait_bounded(&bar[slot], phase, abort_flag, p.wait_limit_ns);
+      if (n == 2) ok = ok && mbar_wait_bounded(&bar[slot1], phase1, abort_flag, p.wait_limit_ns);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      F8Step st;
+      const float2 s0 = slot_scale[slot], s1 = n == 2 ? slot_scale[slot1] : make_float2(1.f, 1.f);
+      st.base[0] = smem_u32(ring + slot * kTile);
+      st.base[1] = smem_u32(ring + slot1 * kTile);
+      st.ks[0] = s0.x, st.vs[0] = s0.y, st.ks[1] = s1.x, st.vs[1] = s1.y;
+      st.dead[0] = __float_as_int(s0.x) == kF8BadTile;
+      st.dead[1] = n == 1 || __float_as_int(s1.x) == kF8BadTile;
+      st.rem = wk.ctx - wk.j * kBlockTokens;
+      cs.step(st, p.q_len, lane);
+      __syncwarp();  // every lane has read the slots
+      if (wi.k < k1) {
+        issue(slot);
+        ++issued;
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty_bar[slot]);
-      if (++stage == p.stages) {
-        stage = 0;
-        phase ^= 1u;
+      if (n == 2 && wi.k < k1) {
+        issue(slot1);
+        ++issued;
       }
+      phase = n == 2 ? phase1 ^ (slot1 + 1 == S ? 1u : 0u) : phase1;
+      slot = n == 2 ? (slot1 + 1 == S ? 0 : slot1 + 1) : slot1;
       if (seg_last || last) {
         // A whole segment's output; a share of one that reaches the unit's
         // end in this warp's drained ring, else in its record.
-        const int nb = wk.nb, st = wk.k - wk.j;
+        const int nb = wk.nb, start = wk.k - wk.j;
         float* rec = nullptr;
-        if (st < k0 || st + nb > k1)
-          rec = last ? reinterpret_cast<float*>(ring + static_cast<size_t>(warp) * p.stages * kTile)
-                     : p.unit_recs + static_cast<size_t>(u) * p.rec_floats;
-        if (last) __syncwarp();
+        if (start < k0 || start + nb > k1)
+          rec = last ? reinterpret_cast<float*>(ring) : p.unit_recs + static_cast<size_t>(u) * p.rec_floats;
         cs.finish(p, rec, wk.b, kvh, first, rows, lane);
         fresh = true;
       }
       if (last) break;
+      wk.k += n - 1;
+      wk.j += n - 1;
       walk_next(wk, prefix, ctxs, B, p.ng);
     }
     cp_async_wait_all();
+    if (!ok && lane == 0) {  // do not leave while copies may still be landing
+      for (int i = max(0, issued - S); i < issued; ++i) {
+        const uint64_t since = global_timer_ns();
+        while (!mbar_try_wait(&bar[i % S], static_cast<uint32_t>((i / S) & 1)) &&
+               global_timer_ns() - since < p.wait_limit_ns) {
+        }
+      }
+    }
   }
   __syncthreads();
 
@@ -769,7 +801,7 @@ __global__ void __launch_bounds__(kF8Threads, 1)
   }
   __syncthreads();
   const int ng = n_groups;
-  for (int i = warp; i < ng * p.rows; i += W + 1) {
+  for (int i = warp; i < ng * p.rows; i += W) {
     const F8Group gr = groups[i / p.rows];
     const int row = i % p.rows;
     int kvh, first;
@@ -777,14 +809,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
     auto at = [&](int j) -> const float* {
       const int u = gr.ua + j;
       const float* rec = gr.en >= unit_begin(sc, u + 1)
-                             ? reinterpret_cast<const float*>(ring + static_cast<size_t>(u - u0) * p.stages * kTile)
+                             ? reinterpret_cast<const float*>(rings + static_cast<size_t>(u - u0) * S * kTile)
                              : p.unit_recs + static_cast<size_t>(u) * p.rec_floats;
       return rec + row * RS;
     };
     float* to = nullptr;
     if (gr.st < A || gr.en > E)
       to = p.cta_recs + (static_cast<size_t>(blockIdx.x) * 2 + (gr.st < A ? 0 : 1)) * p.rec_floats + row * RS;
-    f8_merge_row<D, D / 32, false>(at, gr.ub - gr.ua + 1, 0, lane, p.bf16 != 0, to,
+    f8_merge_row<D, D / 32, false, kBf16>(at, gr.ub - gr.ua + 1, 0, lane, to,
                                    p.out + f8_row_at(p, gr.b, kvh, first + row, D));
   }
 
@@ -822,14 +854,14 @@ __global__ void __launch_bounds__(kF8Threads, 1)
       return p.cta_recs + (static_cast<size_t>(c0 + j) * 2 + (j == 0 ? 1 : 0)) * p.rec_floats + row * RS;
     };
     if (n > 8) {  // many pieces: D / 32 warps share a row
-      for (int i = warp; i < rows * (D / 32); i += W + 1) {
+      for (int i = warp; i < rows * (D / 32); i += W) {
         const int row = i / (D / 32);
-        f8_merge_row<D, 1, true>([&](int j) { return row_at(row, j); }, n, i % (D / 32) * 32, lane, p.bf16 != 0, nullptr,
+        f8_merge_row<D, 1, true, kBf16>([&](int j) { return row_at(row, j); }, n, i % (D / 32) * 32, lane, nullptr,
                                  p.out + f8_row_at(p, gr.b, kvh, first + row, D));
       }
     } else {
-      for (int row = warp; row < rows; row += W + 1)
-        f8_merge_row<D, D / 32, true>([&](int j) { return row_at(row, j); }, n, 0, lane, p.bf16 != 0, nullptr,
+      for (int row = warp; row < rows; row += W)
+        f8_merge_row<D, D / 32, true, kBf16>([&](int j) { return row_at(row, j); }, n, 0, lane, nullptr,
                                       p.out + f8_row_at(p, gr.b, kvh, first + row, D));
     }
   }
