@@ -38,9 +38,10 @@
 namespace pkv {
 
 constexpr int kF8MaxStages = 6;                       // ring slots of a warp
-constexpr int kF8MinTiles = 2;                        // tiles that make a unit worth its merge
+constexpr int kF8MinSlots = 2;                        // slots that make a unit worth its merge
+constexpr int kF8SegSlots = 2;                        // a segment's fixed work, in tiles
+constexpr int kF8W1 = 16, kF8W2 = 8;                  // warps of a CTA with up to 8 rows, with 16
 constexpr int kF8HeaderBytes = 4096;                  // workspace: a counter per CTA
-constexpr int kF8BadTile = 0x7fc0bad0;                 // K scale of a tile whose block id is out of range (a NaN)
 constexpr float kF8RefBelow = 7.f, kF8RefSlack = 14.f;
 
 struct DecodeF8Params {
@@ -97,6 +98,13 @@ __device__ __forceinline__ void ldsm_b8_x2_trans(uint32_t addr, uint32_t& r0, ui
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0,%1,%2,%3}, [%4];"
                : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
                : "r"(addr));
+}
+
+// Adds 1, ordered on both sides at gpu scope (for the CTA, between two of its barriers).
+__device__ __forceinline__ unsigned int add_acq_rel(unsigned int* at) {
+  unsigned int r;
+  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(r) : "l"(at) : "memory");
+  return r;
 }
 
 // 8 x 8 transpose of packed 16-bit pairs: lane (g, t) holds row g, columns 2 t, 2 t + 1 before and after.
@@ -328,49 +336,62 @@ struct F8Consumer {
       }
 
     const uint32_t v0 = st.base[0] + kBlockTokens * D, v1 = st.base[1] + kBlockTokens * D;
-    if (!edge) {
-      pv<false>(v0, 0u, ph[0], pl[0], lane);
-      pv<false>(v1, 0u, ph[1], pl[1], lane);
-    } else {
-      // V bytes behind the context may hold anything: cleared.
-      const int n0 = st.dead[0] ? 0 : st.rem, n1 = st.dead[1] ? 0 : st.rem - kBlockTokens;
-      if (q_len > 1 && (nan_in(v0, keep_bytes(n0, t), lane) || nan_in(v1, keep_bytes(n1, t), lane))) {
-        // A row that does not see a NaN's token would take 0 x NaN: the
-        // product once for each query, over the tokens that it sees.
-#pragma unroll 1
-        for (int hq = 0; hq < q_len; ++hq) {
-          pv<true>(v0, keep_bytes(n0 - hq, t), ph[0], pl[0], lane, hq);
-          pv<true>(v1, keep_bytes(n1 - hq, t), ph[1], pl[1], lane, hq);
-        }
-      } else {
-        pv<true>(v0, keep_bytes(n0, t), ph[0], pl[0], lane);
-        pv<true>(v1, keep_bytes(n1, t), ph[1], pl[1], lane);
-      }
+    if (edge) {
+      clear_behind(v0, st.dead[0] ? 0 : st.rem, lane);
+      if (v1 != v0) clear_behind(v1, st.dead[1] ? 0 : st.rem - kBlockTokens, lane);
+      __syncwarp();
+      if (q_len > 1)
+        for (int i = max(0, st.rem - q_len + 1); i < min(2 * kBlockTokens, st.rem); ++i)
+          if (!st.dead[i >> 4]) nan_of_token(i < kBlockTokens ? v0 : v1, i, st.rem, lane);
+      // The next copy into the slot comes after these writes.
+      asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
+    pv(v0, ph[0], pl[0], lane);
+    pv(v1, ph[1], pl[1], lane);
   }
 
-  // Mask of this lane's four V bytes, of a tile with n tokens.
-  __device__ __forceinline__ static uint32_t keep_bytes(int n, int t) {
-    uint32_t keep = 0;
+  // V rows behind the context (from token n on) may hold anything: zeros.
+  __device__ __forceinline__ static void clear_behind(uint32_t v, int n, int lane) {
+    for (int i = max(n, 0) * (D / 16) + lane; i < kBlockTokens * (D / 16); i += 32)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(v + i * 16), "r"(0u) : "memory");
+  }
+
+  // Several queries: a NaN value of token `i` (of the step), which some rows
+  // do not see, would reach them as 0 x NaN.  It is taken out and put into
+  // the rows that see it.
+  __device__ __forceinline__ void nan_of_token(uint32_t v, int i, int rem, int lane) {
+    const int g = lane >> 2, tok = i & 15;
+    uint32_t w;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w) : "r"(v + tok * D + (lane % (D / 4)) * 4) : "memory");
+    if (!__any_sync(0xffffffffu, (((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) != 0)) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (f8_v_token(4 * t + i) < n) keep |= 0xffu << (8 * i);
-    return keep;
+    for (int mt = 0; mt < MT; ++mt) {
+      const uint32_t at = v + f8_chunk_at<D>(tok, mt) + g;
+      uint32_t c0, c1;
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c0) : "r"(at) : "memory");
+      asm volatile("ld.shared.u8 %0, [%1];" : "=r"(c1) : "r"(at + 8) : "memory");
+      __syncwarp();
+      if ((c0 & 0x7f) == 0x7f) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at), "r"(0u) : "memory");
+      if ((c1 & 0x7f) == 0x7f) asm volatile("st.shared.u8 [%0], %1;" ::"r"(at + 8), "r"(0u) : "memory");
+#pragma unroll
+      for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+          if (i < rem - hide[nr][r]) {
+            if ((c0 & 0x7f) == 0x7f) o[nr][mt][r] = __int_as_float(0x7fc00000);
+            if ((c1 & 0x7f) == 0x7f) o[nr][mt][2 + r] = __int_as_float(0x7fc00000);
+          }
+    }
+    __syncwarp();
   }
 
-  // O^T += V^T P^T of one tile; only_hide >= 0: only rows with that many hidden tokens take it.
-  template <bool kKeep>
-  __device__ __forceinline__ void pv(uint32_t v, uint32_t keep, const uint32_t (&ph)[NR][2], const uint32_t (&pl)[NR][2],
-                                     int lane, int only_hide = -1) {
+  // O^T += V^T P^T of one tile.
+  __device__ __forceinline__ void pv(uint32_t v, const uint32_t (&ph)[NR][2], const uint32_t (&pl)[NR][2], int lane) {
     const int vt = f8_v_token(lane & 15), vc = lane >> 4;
 #pragma unroll
     for (int i = 0; i < D / 32; ++i) {
       uint32_t r[4];
       ldsm_b8_x2_trans(v + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
-      if constexpr (kKeep) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) r[k] &= keep;
-      }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t a0, a1, a2, a3;
@@ -378,35 +399,11 @@ struct F8Consumer {
         f8_unpack4(r[2 * h + 1], a1, a3);
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-          if constexpr (kKeep) {
-            float x[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) x[k] = o[nr][2 * i + h][k];
-            mma_16816<false>(x, a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
-            if constexpr (kRest) mma_16816<false>(x, a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              if (only_hide < 0 || hide[nr][k & 1] == only_hide) o[nr][2 * i + h][k] = x[k];
-          } else {
-            mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
-            if constexpr (kRest) mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
-          }
+          mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, ph[nr][0], ph[nr][1]);
+          if constexpr (kRest) mma_16816<false>(o[nr][2 * i + h], a0, a1, a2, a3, pl[nr][0], pl[nr][1]);
         }
       }
     }
-  }
-
-  __device__ __forceinline__ static bool nan_in(uint32_t v, uint32_t keep, int lane) {
-    const int vt = f8_v_token(lane & 15), vc = lane >> 4;
-    uint32_t found = 0;
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
-      uint32_t r[4];
-      ldsm_b8_x2_trans(v + f8_chunk_at<D>(vt, 2 * i + vc), r[0], r[1], r[2], r[3]);
-#pragma unroll
-      for (int k = 0; k < 4; ++k) found |= ((r[k] & keep & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-    }
-    return __any_sync(0xffffffffu, found != 0);
   }
 
   // The rows' state as a record, or (rec null) their output.
@@ -450,143 +447,239 @@ struct F8Consumer {
   }
 };
 
-// Dims [d0 + DPL lane, + DPL) of one row merged over n pieces, in order:
-//   M = max m_i,  w_i = 2^(m_i - M),  O = sum w_i O_i,  l = sum w_i l_i,
-// online over batches whose loads go out together.  `at(j)`: the row in piece
-// j.  Written to the record row `to`, or normalised to `out`.  kGlobal: the
-// pieces were written by other SMs (read through L2).
-template <int D, int DPL, bool kGlobal, bool kBf16, class At>
-__device__ __forceinline__ void f8_merge_row(const At& at, int n, int d0, int lane, float* to, uint16_t* out) {
-  constexpr int kBatch = DPL == 1 ? 16 : 8;
-  const int dim = d0 + lane * DPL;
-  float M = -INFINITY, L = 0.f, acc[DPL];
+// The n pieces of a segment, in the order of the context: `first`, then base + j
+// stride, and `last` for piece n - 1 where it lies elsewhere (else null).
+struct F8Pieces {
+  const float* first;
+  const float* base;
+  const float* last;
+  int stride;  // floats
+  int n;
+};
+
+// Pieces merged by a warp, online over a few of them at a time whose loads go
+// out together:
+//   M = max m_i,  w_i = 2^(m_i - M),  O = sum w_i O_i,  l = sum w_i l_i.
+// Eight lanes hold a row (D / 8 dims each).  kSplit false: rows row .. row + 3
+// at once, where pieces are few; true: row `row` alone, each group of lanes over
+// every fourth piece, then the groups' states combined, where they are many.
+// Written to the record `to`, or normalised to the output.  The pieces are in
+// shared memory or were written by any SM: generic loads at gpu scope.
+template <int D, bool kBf16, bool kSplit>
+__device__ __noinline__ void f8_merge(const DecodeF8Params& p, const F8Pieces pc, int row, int rows, float* to, int b,
+                                      int kvh, int first_row) {
+  constexpr int DL = D / 8, RS = D + 4, kStep = kSplit ? 4 : 1, kBatch = 2;
+  const int lane = threadIdx.x & 31, group = lane >> 3, dim = (lane & 7) * DL;
+  if (!kSplit) row += group;
+  const bool live = row < rows;
+  const int at = (live ? row : 0) * RS;
+  float M = -INFINITY, L = 0.f, acc[DL];
 #pragma unroll
-  for (int i = 0; i < DPL; ++i) acc[i] = 0.f;
-  for (int j0 = 0; j0 < n; j0 += kBatch) {
-    float mj[kBatch], lj[kBatch], o[kBatch][DPL];
+  for (int i = 0; i < DL; ++i) acc[i] = 0.f;
+#pragma unroll 1
+  for (int j0 = kSplit ? group : 0; j0 < pc.n; j0 += kBatch * kStep) {
+    float mj[kBatch], lj[kBatch], o[kBatch][DL];
 #pragma unroll
     for (int jj = 0; jj < kBatch; ++jj) {
-      const float* r = at(min(j0 + jj, n - 1));
-      if constexpr (kGlobal) {
-        mj[jj] = ld_cg(r + D);
-        lj[jj] = ld_cg(r + D + 1);
-        if constexpr (DPL == 4) {
-          const float4 v = ld_cg4(r + dim);
-          o[jj][0] = v.x, o[jj][1] = v.y, o[jj][2] = v.z, o[jj][3] = v.w;
-        } else if constexpr (DPL == 2) {
-          const float2 v = ld_cg2(r + dim);
-          o[jj][0] = v.x, o[jj][1] = v.y;
-        } else {
-          o[jj][0] = ld_cg(r + dim);
-        }
-      } else {
-        mj[jj] = r[D];
-        lj[jj] = r[D + 1];
+      const int j = min(j0 + jj * kStep, pc.n - 1);  // no branch between loads; a repeated piece gets no weight
+      const float* r = at + (j == 0 ? pc.first : j == pc.n - 1 && pc.last != nullptr ? pc.last : pc.base + j * static_cast<int64_t>(pc.stride));
+      asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(mj[jj]), "=f"(lj[jj]) : "l"(r + D));
 #pragma unroll
-        for (int i = 0; i < DPL; ++i) o[jj][i] = r[dim + i];
-      }
+      for (int i = 0; i < DL; i += 4)
+        asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(o[jj][i]), "=f"(o[jj][i + 1]), "=f"(o[jj][i + 2]), "=f"(o[jj][i + 3])
+                     : "l"(r + dim + i));
     }
+    // -inf: no token seen so far; those pieces' sums are 0 (or NaN, which stays).
     float Mb = M;
 #pragma unroll
-    for (int jj = 0; jj < kBatch; ++jj)
-      if (j0 + jj < n) Mb = fmaxf(Mb, mj[jj]);
-    // -inf: no token seen so far; those pieces' sums are 0 (or NaN, which stays).
+    for (int jj = 0; jj < kBatch; ++jj) Mb = fmaxf(Mb, mj[jj]);  // (a repeated one changes nothing here)
     const float alpha = M == -INFINITY ? 1.f : exp2f(M - Mb);
     L *= alpha;
 #pragma unroll
-    for (int i = 0; i < DPL; ++i) acc[i] *= alpha;
+    for (int i = 0; i < DL; ++i) acc[i] *= alpha;
 #pragma unroll
     for (int jj = 0; jj < kBatch; ++jj) {
-      if (j0 + jj >= n) continue;
+      if (j0 + jj * kStep >= pc.n) continue;
       const float w = mj[jj] == -INFINITY ? 1.f : exp2f(mj[jj] - Mb);
       L = fmaf(w, lj[jj], L);
 #pragma unroll
-      for (int i = 0; i < DPL; ++i) acc[i] = fmaf(w, o[jj][i], acc[i]);
+      for (int i = 0; i < DL; ++i) acc[i] = fmaf(w, o[jj][i], acc[i]);
     }
     M = Mb;
   }
-  if (to != nullptr) {
+  if constexpr (kSplit) {
 #pragma unroll
-    for (int i = 0; i < DPL; ++i) to[dim + i] = acc[i];
-    if (lane == 0 && d0 == 0) {
-      to[D] = M;
-      to[D + 1] = L;
+    for (int x = 8; x < 32; x *= 2) {
+      const float Mb = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+      const float w = M == -INFINITY ? 1.f : exp2f(M - Mb);
+      L *= w;
+      L += __shfl_xor_sync(0xffffffffu, L, x);
+#pragma unroll
+      for (int i = 0; i < DL; ++i) {
+        acc[i] *= w;
+        acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], x);
+      }
+      M = Mb;
     }
+  }
+  if (!live || (kSplit && group > 0)) return;
+  if (to != nullptr) {
+    to += at;
+#pragma unroll
+    for (int i = 0; i < DL; i += 4)
+      *reinterpret_cast<float4*>(to + dim + i) = make_float4(acc[i], acc[i + 1], acc[i + 2], acc[i + 3]);
+    if (dim == 0) *reinterpret_cast<float2*>(to + D) = make_float2(M, L);
     return;
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
-  uint32_t w[2];
+  uint16_t* out = p.out + f8_row_at(p, b, kvh, first_row + row, D) + dim;
 #pragma unroll
-  for (int i = 0; i < (DPL + 1) / 2; ++i) {
-    const float x = acc[2 * i] * inv, z = DPL > 1 ? acc[(2 * i + 1) % DPL] * inv : 0.f;
-    w[i] = pack2<kBf16>(x, z);
+  for (int i = 0; i < DL; i += 4)
+    *reinterpret_cast<uint2*>(out + i) = make_uint2(pack2<kBf16>(acc[i] * inv, acc[i + 1] * inv),
+                                                    pack2<kBf16>(acc[i + 2] * inv, acc[i + 3] * inv));
+}
+
+// Work is counted in slots: a segment has kF8SegSlots for its start and end (Q,
+// the first maxima, the output), then one for each tile.  A unit's range of
+// slots begins at its share of them, or at the segment's first slot where that
+// share begins before the segment's second tile.
+struct F8Walk {
+  int b, hg;   // segment
+  int st, nb;  // its first slot, its tiles
+  int j;       // tile
+};
+
+// The segment of slot k.
+__device__ __forceinline__ F8Walk f8_find(const int* prefix, const int* ctxs, int B, int k) {
+  int lo = 0, hi = B;  // prefix[lo] <= k < prefix[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (prefix[mid] <= k) lo = mid; else hi = mid;
   }
-  if constexpr (DPL == 4)
-    *reinterpret_cast<uint2*>(out + dim) = make_uint2(w[0], w[1]);
-  else if constexpr (DPL == 2)
-    *reinterpret_cast<uint32_t*>(out + dim) = w[0];
-  else
-    out[dim] = static_cast<uint16_t>(w[0]);
+  F8Walk w;
+  w.b = lo;
+  w.nb = (ctxs[lo] + kBlockTokens - 1) / kBlockTokens;
+  const int local = k - prefix[lo];
+  w.hg = local / (w.nb + kF8SegSlots);
+  w.st = k - local + w.hg * (w.nb + kF8SegSlots);
+  w.j = max(0, k - w.st - kF8SegSlots);
+  return w;
+}
+
+__device__ __forceinline__ void f8_next_segment(F8Walk& w, const int* prefix, const int* ctxs, int B, int ng) {
+  w.st += w.nb + kF8SegSlots;
+  w.j = 0;
+  if (++w.hg == ng) {
+    w.hg = 0;
+    do {
+      ++w.b;
+    } while (w.b < B && prefix[w.b + 1] == prefix[w.b]);
+    w.nb = w.b < B ? (ctxs[w.b] + kBlockTokens - 1) / kBlockTokens : 0;
+  }
+}
+
+// Where unit u's slots begin.
+__device__ __forceinline__ int f8_unit_begin(const Sched& sc, int u, const int* prefix, const int* ctxs, int B) {
+  const int k = unit_begin(sc, u);
+  if (u == 0 || u >= sc.U) return k;
+  const F8Walk w = f8_find(prefix, ctxs, B, k);
+  return w.j == 0 ? w.st : k;
 }
 
 // Rows of a segment that this CTA holds in several units, or shares with other CTAs.
 struct F8Group {
-  int b, hg, st, en;  // the segment's tiles [st, en)
+  int b, hg, st, en;  // the segment's slots [st, en)
   int ua, ub;         // first and last unit of this CTA with a piece of it
+  int c0, n_ctas;     // its CTAs: the one of its first tile, how many
+  int kvh, first, rows;
 };
 
-// Warps of a CTA, each a unit.
-__host__ __device__ constexpr int f8_warps(int NR) { return NR == 1 ? 12 : 8; }
+// The CTA's segments with a share in several units or CTAs, in order: of the
+// candidates that one comes from before the CTA, and one starts in each unit and
+// goes on behind it.  By one warp, while the first copies are under way.
+template <int W>
+__device__ __noinline__ void f8_find_groups(const DecodeF8Params& p, const Sched sc, int per_cta, int u0, int n_units,
+                                            const int* bnd, const int* prefix, const int* ctxs, F8Group* groups,
+                                            int* n_groups) {
+  static_assert(W < 32, "a lane for each candidate");
+  const int lane = threadIdx.x & 31, A = bnd[0], E = bnd[n_units];
+  bool valid = false;
+  F8Group gr;
+  if (lane <= n_units && A < E) {
+    const int w = max(0, lane - 1), k = lane == 0 ? A : bnd[w + 1] - 1;
+    const F8Walk f = f8_find(prefix, ctxs, p.batch, k);
+    gr.b = f.b;
+    gr.hg = f.hg;
+    gr.st = f.st;
+    gr.en = f.st + f.nb + kF8SegSlots;
+    valid = lane == 0 ? gr.st < A : bnd[w] < bnd[w + 1] && gr.st >= bnd[w] && gr.en > bnd[w + 1];
+    const int last = unit_of_tile(sc, gr.en - 1);
+    gr.ua = w;
+    gr.ub = min(last - u0, n_units - 1);
+    if (lane == 0)  // units in front of the first tile have no piece
+      while (bnd[gr.ua + 1] == A) ++gr.ua;
+    gr.c0 = unit_of_tile(sc, gr.st + kF8SegSlots) / per_cta;
+    gr.n_ctas = last / per_cta - gr.c0 + 1;
+    gr.kvh = gr.hg / p.nseg;
+    gr.first = (gr.hg - gr.kvh * p.nseg) * p.rows;
+    gr.rows = min(p.rows, p.total_rows - gr.first);
+  }
+  const uint32_t mask = __ballot_sync(0xffffffffu, valid);
+  if (valid) groups[__popc(mask & ((1u << lane) - 1u))] = gr;
+  if (lane == 0) *n_groups = __popc(mask);
+}
 
-// Shared memory: each warp's ring, its Q rows, a scale pair and a barrier of each slot; lengths.
+// Warps of a CTA, each a unit.
+__host__ __device__ constexpr int f8_warps(int NR) { return NR == 1 ? kF8W1 : kF8W2; }
+
+// Shared memory: each warp's ring, its Q rows; a barrier, a scale pair and a flag of each ring slot; lengths.
 __host__ __device__ constexpr size_t f8_smem_bytes(int D, int W, int stages, int rows, int batch) {
-  return 1024 + static_cast<size_t>(W) * (stages * (f8_tile_bytes(D) + 16) + rows * D * 2) + 16 +
+  return 1024 + static_cast<size_t>(W) * (stages * (f8_tile_bytes(D) + 20) + rows * D * 2) + 16 +
          (2 * static_cast<size_t>(batch) + 1) * 4;
 }
 
 template <int D, int NR, bool kBf16>
 __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
-    pkv_decode_f8_kernel(const __grid_constant__ CUtensorMap tm, const DecodeF8Params p) {
+    pkv_decode_f8_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ DecodeF8Params p) {
   constexpr int kTile = f8_tile_bytes(D);
   constexpr int W = f8_warps(NR), kThreads = W * 32;
   using Consumer = F8Consumer<D, NR, kBf16>;
-  constexpr int RS = Consumer::RS;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* rings = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  const int S = p.stages, q_bytes = p.rows * D * 2;
-  uint8_t* qbufs = rings + static_cast<size_t>(W) * S * kTile;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(qbufs + W * q_bytes);  // [W][S]: the slot's copies have landed
-  float2* slot_scales = reinterpret_cast<float2*>(bars + W * S);      // [W][S]
-  volatile int* abort_flag = reinterpret_cast<int*>(slot_scales + W * S);
-  int* prefix = const_cast<int*>(abort_flag) + 4;  // [batch + 1]
+  const int S = p.stages, q_bytes = p.rows * D * 2, n_slots = W * S;
+  uint8_t* qbufs = rings + static_cast<size_t>(n_slots) * kTile;
+  uint64_t* full_bar = reinterpret_cast<uint64_t*>(qbufs + W * q_bytes);  // [W][S]: the slot's copies have landed
+  float2* slot_scale = reinterpret_cast<float2*>(full_bar + n_slots);
+  int* slot_bad = reinterpret_cast<int*>(slot_scale + n_slots);
+  volatile int* abort_flag = slot_bad + n_slots;
+  int* prefix = const_cast<int*>(abort_flag) + 4;  // [batch + 1]: slots before each sequence
   int* ctxs = prefix + p.batch + 1;                // [batch]
   __shared__ int warp_sums[W];
+  __shared__ int bnd[W + 1];  // where this CTA's units begin
   __shared__ F8Group groups[W + 1];
   __shared__ int n_groups;
   __shared__ int last_of[2];  // this CTA finishes: the segment from before it, the one that goes on behind it
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int B = p.batch;
-  uint8_t* ring = rings + static_cast<size_t>(warp) * S * kTile;  // this warp's
-  uint64_t* bar = bars + warp * S;
-  float2* slot_scale = slot_scales + warp * S;
 
-  if (threadIdx.x == 0) {
-    tma_prefetch_desc(&tm);
-    *abort_flag = 0;
-  }
-  if (lane == 0) {
-    for (int i = 0; i < S; ++i) mbar_init(&bar[i], 2);  // the codes' bytes, and the scales
+  if (threadIdx.x < n_slots) {
+    mbar_init(&full_bar[threadIdx.x], 2);  // the codes' bytes, and the scales
     mbar_fence_init();
   }
+  if (threadIdx.x == 0) {
+    *abort_flag = 0;
+    tma_prefetch_desc(&tm);
+  }
 
-  // Tiles before each sequence.
   {
     const int per = (B + kThreads - 1) / kThreads;
     const int lo = min(B, static_cast<int>(threadIdx.x) * per), hi = min(B, lo + per);
     const int max_ctx = p.max_blocks_per_seq * kBlockTokens;
+    auto slots_of = [&](int c) { return c > 0 ? ((c + kBlockTokens - 1) / kBlockTokens + kF8SegSlots) * p.ng : 0; };
     int local = 0;
     for (int b = lo; b < hi; ++b) {
       const int c0 = __ldg(p.context_lens + b);
@@ -594,7 +687,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
       if (c > 0 && c < p.q_len) c = 0;
       if (c != c0) flag_error(PKV_DEVERR_CONTEXT);
       ctxs[b] = c;
-      local += ((c + kBlockTokens - 1) / kBlockTokens) * p.ng;
+      local += slots_of(c);
     }
     int incl = local;
 #pragma unroll
@@ -609,7 +702,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     int run = base + incl - local;
     for (int b = lo; b < hi; ++b) {
       prefix[b] = run;
-      run += ((ctxs[b] + kBlockTokens - 1) / kBlockTokens) * p.ng;
+      run += slots_of(ctxs[b]);
     }
     if (threadIdx.x == kThreads - 1) prefix[B] = base + incl;
   }
@@ -624,9 +717,13 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     }
 
   const int T = prefix[B];
-  const Sched sc = make_sched(T, min(static_cast<int>(gridDim.x) * W, max(1, T / kF8MinTiles)), 0, 1000);
-  const int u0 = blockIdx.x * W, u_end = min(sc.U, u0 + W);  // this CTA's units
-  if (T == 0 || u0 >= sc.U) return;
+  const Sched sc = make_sched(T, min(static_cast<int>(gridDim.x) * W, max(1, T / kF8MinSlots)), 0, 1000);
+  // A small problem's units go over all CTAs, fewer to each.
+  const int per_cta = (sc.U + gridDim.x - 1) / static_cast<int>(gridDim.x);
+  const int u0 = blockIdx.x * per_cta, n_units = min(sc.U - u0, per_cta);  // this CTA's units
+  if (T == 0 || n_units <= 0) return;
+  if (threadIdx.x <= n_units) bnd[lane] = f8_unit_begin(sc, u0 + lane, prefix, ctxs, B);
+  __syncthreads();
 
   // Rows of segment hg of a sequence: kv head, first of its rows, how many.
   auto seg_rows = [&](int hg, int& kvh, int& first) {
@@ -635,23 +732,36 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     return min(p.rows, p.total_rows - first);
   };
 
-  if (u0 + warp < u_end) {
-    const int u = u0 + warp, k0 = unit_begin(sc, u), k1 = unit_begin(sc, u + 1);
+  if (warp < n_units && bnd[warp] < bnd[warp + 1]) {
+    const int k0 = bnd[warp], k1 = bnd[warp + 1], slot_begin = warp * S, slot_end = slot_begin + S;
     const uint64_t policy = p.nseg == 1 ? l2_policy_evict_first() : l2_policy_evict_normal();
 
-    // Issue side: the warp copies its own tiles, S ahead of their use.  Block
-    // ids come in windows of 32 (lane i holds entry wj + i of sequence wb's
-    // table); the window that is needed next is loaded when one is taken.
-    Walk wi;
-    walk_begin(wi, prefix, ctxs, B, k0, k1);
+    uint8_t* ring = rings + static_cast<size_t>(warp) * S * kTile;
+    uint8_t* qbuf = qbufs + warp * q_bytes;
+    auto fetch_q = [&](int b, int hg) {
+      int kvh, first;
+      const int rows = seg_rows(hg, kvh, first);
+      constexpr int kChunks = D / 8;
+      for (int i = lane; i < rows * kChunks; i += 32)
+        cp_async_16(qbuf + i * 16, p.q + f8_row_at(p, b, kvh, first + i / kChunks, D) + (i % kChunks) * 8);
+      cp_async_commit();
+    };
+    F8Walk wk = f8_find(prefix, ctxs, B, k0);
+    fetch_q(wk.b, wk.hg);  // in front of the copies that fill the memory's queues
+
+    // Issue side: the warp copies its own tiles, a ring ahead of their use.
+    // Block ids come in windows of 32 (lane i holds entry wj + i of sequence
+    // wb's table); the window that is needed next is loaded when one is taken.
+    F8Walk wi = wk;
+    int left = k1 - max(k0, wi.st + kF8SegSlots);  // slots from tile wi.j on; a tile while positive
     auto table = [&](int b, int j) {
       const int at = j + lane;
       return at < p.max_blocks_per_seq ? __ldg(p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq + at) : -1;
     };
     int wb = -1, wj = 0, ids = 0, nxb = -1, nxj = 0, nx_ids = 0;
     auto window = [&]() {
-      if (wi.b == wb && wi.j >= wj && wi.j < wj + 32) return;
-      if (wi.b == nxb && wi.j >= nxj && wi.j < nxj + 32) {
+      if (wi.b == wb && static_cast<unsigned>(wi.j - wj) < 32u) return;
+      if (wi.b == nxb && static_cast<unsigned>(wi.j - nxj) < 32u) {
         wb = nxb, wj = nxj, ids = nx_ids;
       } else {
         wb = wi.b, wj = wi.nb <= 32 ? 0 : wi.j;
@@ -667,157 +777,142 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
       }
       if (nxb < B) nx_ids = table(nxb, nxj);
     };
-    auto issue = [&](int slot) {
-      window();
-      const int phys = __shfl_sync(0xffffffffu, ids, wi.j - wj);
-      if (lane == 0) {
-        if (phys < 0 || phys >= p.num_blocks) {  // nothing is copied; a NaN K scale marks the tile
-          flag_error(PKV_DEVERR_BLOCK_ID);
-          slot_scale[slot] = make_float2(__int_as_float(kF8BadTile), 0.f);
-          mbar_arrive(&bar[slot]);
-          mbar_arrive(&bar[slot]);
-        } else {
-          const int at = phys * p.n_kv_heads + wi.hg / p.nseg;
-          mbar_arrive_expect_tx(&bar[slot], kTile);
-          tma_load_3d_hint(ring + slot * kTile, &tm, &bar[slot], at, policy);
-          cp_async_8(&slot_scale[slot], p.scales + at);
-          cp_async_arrive(&bar[slot]);
+    // Tile wi.j + i into a slot, by one lane.
+    auto copy = [&](int phys, int slot) {
+      const bool bad = phys < 0 || phys >= p.num_blocks;
+      slot_bad[slot] = bad;  // published by the arrivals
+      if (bad) {             // nothing is copied; the tile is left out
+        flag_error(PKV_DEVERR_BLOCK_ID);
+        mbar_arrive(&full_bar[slot]);
+        mbar_arrive(&full_bar[slot]);
+      } else {
+        const int at = phys * p.n_kv_heads + wi.hg / p.nseg;
+        mbar_arrive_expect_tx(&full_bar[slot], kTile);
+        tma_load_3d_hint(rings + static_cast<size_t>(slot) * kTile, &tm, &full_bar[slot], at, policy);
+        cp_async_8(&slot_scale[slot], p.scales + at);
+        cp_async_arrive(&full_bar[slot]);
+      }
+    };
+    // The next tiles into n slots from `slot` on, a lane for each.
+    int issued = 0;
+    auto issue = [&](int slot, int n) {
+      while (n > 0 && left > 0) {
+        window();
+        const int off = wi.j - wj, k = min(min(n, left), min(wi.nb - wi.j, 32 - off));
+        const int phys = __shfl_sync(0xffffffffu, ids, off + lane);
+        if (lane < k) copy(phys, slot + lane < slot_end ? slot + lane : slot + lane - S);
+        slot += k;
+        if (slot >= slot_end) slot -= S;
+        n -= k;
+        issued += k;
+        left -= k;
+        wi.j += k;
+        if (wi.j == wi.nb) {
+          f8_next_segment(wi, prefix, ctxs, B, p.ng);
+          left -= kF8SegSlots;
         }
       }
-      walk_next(wi, prefix, ctxs, B, p.ng);
     };
-    int issued = 0;
-    for (; issued < S && wi.k < k1; ++issued) issue(issued);
+    issue(slot_begin, S);
+    if (warp == W - 1) f8_find_groups<W>(p, sc, per_cta, u0, n_units, bnd, prefix, ctxs, groups, &n_groups);
 
-    uint8_t* qbuf = qbufs + warp * q_bytes;
-    auto fetch_q = [&](int b, int hg) {
-      int kvh, first;
-      const int rows = seg_rows(hg, kvh, first);
-      constexpr int kChunks = D / 8;
-      for (int i = lane; i < rows * kChunks; i += 32)
-        cp_async_16(qbuf + i * 16, p.q + f8_row_at(p, b, kvh, first + i / kChunks, D) + (i % kChunks) * 8);
-      cp_async_commit();
-    };
-    Walk wk;
-    walk_begin(wk, prefix, ctxs, B, k0, k1);
-    fetch_q(wk.b, wk.hg);
     Consumer cs;
-    int slot = 0, kvh = 0, first = 0, rows = 0;
+    int slot = slot_begin;
     uint32_t phase = 0;
-    bool fresh = true, ok = true;
+    bool ok = true;
+    // Segment by segment; `end` is the first tile that is not this unit's.
     while (true) {
-      if (fresh) {
-        fresh = false;
-        rows = seg_rows(wk.hg, kvh, first);
-        cp_async_wait_all();
-        __syncwarp();
-        cs.begin(p, qbuf, first, rows, lane);
-        __syncwarp();
+      int kvh, first;
+      const int rows = seg_rows(wk.hg, kvh, first);
+      const int end = min(wk.nb, k1 - wk.st - kF8SegSlots), ctx = ctxs[wk.b];
+      F8Walk nx = wk;
+      f8_next_segment(nx, prefix, ctxs, B, p.ng);
+      const bool more = nx.st < k1;
+      cp_async_wait_all();
+      __syncwarp();
+      cs.begin(p, qbuf, first, rows, lane);
+      __syncwarp();
+      if (more) fetch_q(nx.b, nx.hg);  // the next segment's Q, behind this one's tiles
+#pragma unroll 1
+      for (int j = wk.j; j < end; j += 2) {
+        const bool two = j + 1 < end;
+        const int slot0 = slot;
+        ok = mbar_wait_bounded(&full_bar[slot0], phase, abort_flag, p.wait_limit_ns);
+        if (++slot == slot_end) {
+          slot -= S;
+          phase ^= 1u;
+        }
+        const int slot1 = slot;
+        if (two) {
+          ok = ok && mbar_wait_bounded(&full_bar[slot1], phase, abort_flag, p.wait_limit_ns);
+          if (++slot == slot_end) {
+            slot -= S;
+            phase ^= 1u;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        F8Step st;
+        // Without a second tile the first one stands in for it (the next
+        // slot's copy may be under way), dead.
+        st.base[0] = smem_u32(rings) + slot0 * kTile;
+        st.base[1] = two ? smem_u32(rings) + slot1 * kTile : st.base[0];
+        st.dead[0] = slot_bad[slot0] != 0;
+        st.dead[1] = !two || slot_bad[slot1] != 0;
+        const float2 one = make_float2(1.f, 1.f);
+        const float2 s0 = st.dead[0] ? one : slot_scale[slot0], s1 = st.dead[1] ? one : slot_scale[slot1];
+        st.ks[0] = s0.x, st.vs[0] = s0.y, st.ks[1] = s1.x, st.vs[1] = s1.y;
+        st.rem = ctx - j * kBlockTokens;
+        cs.step(st, p.q_len, lane);
+        __syncwarp();  // every lane has read the slots
+        issue(slot0, two ? 2 : 1);
       }
-      const int n = min(min(2, wk.nb - wk.j), k1 - wk.k);  // tiles of this step
-      const bool last = wk.k + n >= k1, seg_last = wk.j + n >= wk.nb;
-      if (seg_last && !last) {  // the next segment's Q
-        Walk nx = wk;
-        nx.j = nx.nb - 1;
-        walk_next(nx, prefix, ctxs, B, p.ng);
-        fetch_q(nx.b, nx.hg);
-      }
-      const int slot1 = slot + 1 == S ? 0 : slot + 1;
-      const uint32_t phase1 = phase ^ (slot1 == 0 ? 1u : 0u);
-      ok = mbar_wait_bounded(&bar[slot], phase, abort_flag, p.wait_limit_ns);
-      if (n == 2) ok = ok && mbar_wait_bounded(&bar[slot1], phase1, abort_flag, p.wait_limit_ns);
-      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      F8Step st;
-      const float2 s0 = slot_scale[slot], s1 = n == 2 ? slot_scale[slot1] : make_float2(1.f, 1.f);
-      st.base[0] = smem_u32(ring + slot * kTile);
-      st.base[1] = smem_u32(ring + slot1 * kTile);
-      st.ks[0] = s0.x, st.vs[0] = s0.y, st.ks[1] = s1.x, st.vs[1] = s1.y;
-      st.dead[0] = __float_as_int(s0.x) == kF8BadTile;
-      st.dead[1] = n == 1 || __float_as_int(s1.x) == kF8BadTile;
-      st.rem = wk.ctx - wk.j * kBlockTokens;
-      cs.step(st, p.q_len, lane);
-      __syncwarp();  // every lane has read the slots
-      if (wi.k < k1) {
-        issue(slot);
-        ++issued;
-      }
-      if (n == 2 && wi.k < k1) {
-        issue(slot1);
-        ++issued;
-      }
-      phase = n == 2 ? phase1 ^ (slot1 + 1 == S ? 1u : 0u) : phase1;
-      slot = n == 2 ? (slot1 + 1 == S ? 0 : slot1 + 1) : slot1;
-      if (seg_last || last) {
-        // A whole segment's output; a share of one that reaches the unit's
-        // end in this warp's drained ring, else in its record.
-        const int nb = wk.nb, start = wk.k - wk.j;
-        float* rec = nullptr;
-        if (start < k0 || start + nb > k1)
-          rec = last ? reinterpret_cast<float*>(ring) : p.unit_recs + static_cast<size_t>(u) * p.rec_floats;
-        cs.finish(p, rec, wk.b, kvh, first, rows, lane);
-        fresh = true;
-      }
-      if (last) break;
-      wk.k += n - 1;
-      wk.j += n - 1;
-      walk_next(wk, prefix, ctxs, B, p.ng);
+      // A whole segment's output; a share of one that reaches the unit's end
+      // in this warp's drained ring, else in its record.
+      float* rec = nullptr;
+      if (wk.st < k0 || nx.st > k1)
+        rec = nx.st >= k1 ? reinterpret_cast<float*>(ring) : p.unit_recs + static_cast<size_t>(u0 + warp) * p.rec_floats;
+      cs.finish(p, rec, wk.b, kvh, first, rows, lane);
+      if (!more) break;
+      wk = nx;
     }
     cp_async_wait_all();
-    if (!ok && lane == 0) {  // do not leave while copies may still be landing
+    if (!ok && lane == 0)  // do not leave while copies may still be landing
       for (int i = max(0, issued - S); i < issued; ++i) {
         const uint64_t since = global_timer_ns();
-        while (!mbar_try_wait(&bar[i % S], static_cast<uint32_t>((i / S) & 1)) &&
+        while (!mbar_try_wait(&full_bar[slot_begin + i % S], static_cast<uint32_t>((i / S) & 1)) &&
                global_timer_ns() - since < p.wait_limit_ns) {
         }
       }
-    }
+  } else if (warp == W - 1) {
+    f8_find_groups<W>(p, sc, per_cta, u0, n_units, bnd, prefix, ctxs, groups, &n_groups);
   }
   __syncthreads();
 
   // ---------------- the CTA's shared segments ----------------
-  // Candidates: the segment that comes from before the CTA, and for each unit
-  // the segment that starts in it and goes on behind it.
-  const int A = unit_begin(sc, u0), E = unit_begin(sc, u_end);
-  if (warp == 0) {
-    bool valid = false;
-    F8Group gr;
-    if (lane <= u_end - u0) {
-      const int u = u0 + max(0, lane - 1);
-      const int k = lane == 0 ? A : unit_begin(sc, u + 1) - 1;
-      Walk w;
-      walk_begin(w, prefix, ctxs, B, k, k + 1);
-      gr.b = w.b;
-      gr.hg = w.hg;
-      gr.st = k - w.j;
-      gr.en = gr.st + w.nb;
-      gr.ua = u;
-      gr.ub = min(unit_of_tile(sc, gr.en - 1), u_end - 1);
-      valid = lane == 0 ? gr.st < A : gr.st >= unit_begin(sc, u) && gr.en > k + 1;
+  const int A = bnd[0], E = bnd[n_units], ng = n_groups;
+  // A warp a row while the warps suffice (long contexts: one or two groups of
+  // many pieces), else four rows a warp (many groups of two pieces).
+  const bool split = ng * p.rows <= W;
+  const int items = split ? p.rows : (p.rows + 3) / 4;
+  for (int i = warp; i < ng * items; i += W) {
+    const F8Group& gr = groups[i / items];
+    F8Pieces pc;  // in the rings; the last one in its unit's record if more follows it there
+    pc.n = gr.ub - gr.ua + 1;
+    pc.stride = S * kTile / 4;
+    pc.base = pc.first = reinterpret_cast<const float*>(rings) + static_cast<size_t>(gr.ua) * pc.stride;
+    pc.last = nullptr;
+    if (gr.en < bnd[gr.ub + 1]) {
+      pc.last = p.unit_recs + static_cast<size_t>(u0 + gr.ub) * p.rec_floats;
+      if (pc.n == 1) pc.first = pc.last;
     }
-    const uint32_t mask = __ballot_sync(0xffffffffu, valid);
-    if (valid) groups[__popc(mask & ((1u << lane) - 1u))] = gr;
-    if (lane == 0) n_groups = __popc(mask);
-  }
-  __syncthreads();
-  const int ng = n_groups;
-  for (int i = warp; i < ng * p.rows; i += W) {
-    const F8Group gr = groups[i / p.rows];
-    const int row = i % p.rows;
-    int kvh, first;
-    if (row >= seg_rows(gr.hg, kvh, first)) continue;
-    auto at = [&](int j) -> const float* {
-      const int u = gr.ua + j;
-      const float* rec = gr.en >= unit_begin(sc, u + 1)
-                             ? reinterpret_cast<const float*>(rings + static_cast<size_t>(u - u0) * S * kTile)
-                             : p.unit_recs + static_cast<size_t>(u) * p.rec_floats;
-      return rec + row * RS;
-    };
     float* to = nullptr;
-    if (gr.st < A || gr.en > E)
-      to = p.cta_recs + (static_cast<size_t>(blockIdx.x) * 2 + (gr.st < A ? 0 : 1)) * p.rec_floats + row * RS;
-    f8_merge_row<D, D / 32, false, kBf16>(at, gr.ub - gr.ua + 1, 0, lane, to,
-                                   p.out + f8_row_at(p, gr.b, kvh, first + row, D));
+    if (gr.st < A || gr.en > E) to = p.cta_recs + (static_cast<size_t>(blockIdx.x) * 2 + (gr.st < A ? 0 : 1)) * p.rec_floats;
+    if (split)
+      f8_merge<D, kBf16, true>(p, pc, i % items, gr.rows, to, gr.b, gr.kvh, gr.first);
+    else
+      f8_merge<D, kBf16, false>(p, pc, i % items * 4, gr.rows, to, gr.b, gr.kvh, gr.first);
   }
 
   // ---------------- segments shared with other CTAs ----------------
@@ -825,44 +920,37 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   const bool from_before = ng > 0 && groups[0].st < A;
   const bool goes_on = ng > 0 && groups[ng - 1].en > E && groups[ng - 1].st >= A;
   if (!from_before && !goes_on) return;
-  __threadfence();
   __syncthreads();
   if (threadIdx.x < 2) {
     int fin = 0;
     if (threadIdx.x == 0 ? from_before : goes_on) {
       const F8Group& gr = groups[threadIdx.x == 0 ? 0 : ng - 1];
-      const int c0 = unit_of_tile(sc, gr.st) / W, n = unit_of_tile(sc, gr.en - 1) / W - c0 + 1;
-      const unsigned int before = atomicAdd(p.counters + c0, 1u);
-      if (before >= static_cast<unsigned int>(n)) flag_error(PKV_DEVERR_SCHEDULE);
-      if (before + 1 >= static_cast<unsigned int>(n)) {
+      const unsigned int n = static_cast<unsigned int>(gr.n_ctas);
+      const unsigned int before = add_acq_rel(p.counters + gr.c0);  // after every record of this CTA, before any it reads
+      if (before >= n) flag_error(PKV_DEVERR_SCHEDULE);
+      if (before + 1 >= n) {
         fin = 1;
-        p.counters[c0] = 0;
+        p.counters[gr.c0] = 0;
       }
     }
     last_of[threadIdx.x] = fin;
-    __threadfence();
   }
   __syncthreads();
 #pragma unroll 1
   for (int k = 0; k < 2; ++k) {
     if (last_of[k] == 0) continue;
-    const F8Group gr = groups[k == 0 ? 0 : ng - 1];
-    const int c0 = unit_of_tile(sc, gr.st) / W, n = unit_of_tile(sc, gr.en - 1) / W - c0 + 1;
-    int kvh, first;
-    const int rows = seg_rows(gr.hg, kvh, first);
-    auto row_at = [&](int row, int j) -> const float* {  // the first CTA's share goes on behind it, the others' come from before
-      return p.cta_recs + (static_cast<size_t>(c0 + j) * 2 + (j == 0 ? 1 : 0)) * p.rec_floats + row * RS;
-    };
-    if (n > 8) {  // many pieces: D / 32 warps share a row
-      for (int i = warp; i < rows * (D / 32); i += W) {
-        const int row = i / (D / 32);
-        f8_merge_row<D, 1, true, kBf16>([&](int j) { return row_at(row, j); }, n, i % (D / 32) * 32, lane, nullptr,
-                                 p.out + f8_row_at(p, gr.b, kvh, first + row, D));
-      }
+    const F8Group& gr = groups[k == 0 ? 0 : ng - 1];
+    F8Pieces pc;  // the first CTA's share goes on behind it, the others' come from before
+    pc.n = gr.n_ctas;
+    pc.stride = 2 * p.rec_floats;
+    pc.base = p.cta_recs + static_cast<size_t>(gr.c0) * pc.stride;
+    pc.first = pc.base + p.rec_floats;
+    pc.last = nullptr;
+    if (pc.n > 4) {
+      for (int i = warp; i < gr.rows; i += W) f8_merge<D, kBf16, true>(p, pc, i, gr.rows, nullptr, gr.b, gr.kvh, gr.first);
     } else {
-      for (int row = warp; row < rows; row += W)
-        f8_merge_row<D, D / 32, true, kBf16>([&](int j) { return row_at(row, j); }, n, 0, lane, nullptr,
-                                      p.out + f8_row_at(p, gr.b, kvh, first + row, D));
+      for (int i = warp * 4; i < gr.rows; i += W * 4)
+        f8_merge<D, kBf16, false>(p, pc, i, gr.rows, nullptr, gr.b, gr.kvh, gr.first);
     }
   }
 }
