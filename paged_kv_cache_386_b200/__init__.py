@@ -614,71 +614,102 @@ def rotary_table(max_positions: int, rot_dim: int, theta: float = 10000.0, devic
     return torch.cat((angle.cos(), angle.sin()), 1).float()
 
 
-def _heads(t: torch.Tensor, name: str) -> tuple[int, int]:
+# The calls below are host-bound at a decode step's sizes, so their checks read
+# each tensor's shape and strides once, and the device is only switched when
+# another one is current.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
+def _launch(entry: str, index: int, stream, *args) -> None:
+    """Calls C entry point `entry`, whose last argument is the stream, on device `index`."""
+    fn = getattr(_lib or _load(), entry)
+    if stream is not None:
+        raw = _stream(stream)
+    if torch.cuda.current_device() == index:
+        status = fn(*args, _raw_stream(index) if stream is None else raw)
+    else:
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index) if stream is None else raw)
+    if status != PKV_OK:
+        raise PagedKVError(status, entry)
+
+
+def _on_device(index: int, *tensors) -> None:
+    if index < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"every tensor must be on cuda:{index} (found {t.device})")
+
+
+def _flat(t: torch.Tensor, name: str) -> int:
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _heads(t: torch.Tensor, n: int, h: int, d: int, name: str) -> tuple[int, int]:
     """Pointer and token stride (elements) of ``[num_tokens, heads, head_dim]``
     whose heads are contiguous within a token."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    n, h, d = t.shape
-    if (d > 1 and t.stride(2) != 1) or (h > 1 and t.stride(1) != d):
+    if t.shape != (n, h, d):
+        raise ValueError(f"{name} must be [num_tokens, heads, head_dim] = {(n, h, d)}, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of one token must be contiguous")
-    return t.data_ptr(), (t.stride(0) if n > 1 else h * d)
+    return t.data_ptr(), (s0 if n > 1 else h * d)
 
 
-def _check_new_tokens(k, v, slot_mapping, n_kv: int, d: int) -> None:
-    if k.dim() != 3 or tuple(k.shape[1:]) != (n_kv, d) or tuple(v.shape) != tuple(k.shape):
-        raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim] with the cache's heads")
+def _check_kv(k, v, slot_mapping) -> int:
     if k.dtype not in _DTYPE or v.dtype != k.dtype:
         raise ValueError("k and v must both be float32, float16 or bfloat16")
-    if slot_mapping.dtype != torch.int64 or tuple(slot_mapping.shape) != (k.shape[0],):
+    if k.dim() != 3:
+        raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim]")
+    n = k.shape[0]
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must be int64 [num_tokens]")
-
-
-def _check_rope(k, positions, cos_sin, q, q_out) -> None:
-    if positions.dtype != torch.int64 or tuple(positions.shape) != (k.shape[0],):
-        raise ValueError("positions must be int64 [num_tokens]")
-    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
-        raise ValueError("cos_sin must be float32 [max_positions, rot_dim] (rotary_table)")
-    if q is None:
-        if q_out is not None:
-            raise ValueError("q_out without q")
-        return
-    if q.dim() != 3 or q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or q.dtype != k.dtype:
-        raise ValueError("q must be [num_tokens, n_q_heads, head_dim] of k's dtype")
-    if q_out is not None and (tuple(q_out.shape) != tuple(q.shape) or q_out.dtype != q.dtype):
-        raise ValueError("q_out must have q's shape and dtype")
+    return n
 
 
 def _empty_for(like: torch.Tensor, stream) -> torch.Tensor:
     """A contiguous output that belongs to the stream that writes it."""
     if stream is None:
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(_stream(stream), device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(like.shape, dtype=like.dtype, device=like.device)
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
-def _append_rope(entry: str, k, v, positions, cos_sin, slot_mapping, cache, scales, n_blocks, q, q_out, interleaved,
-                 block_size, stream):
-    lib = _load()
-    n_kv, d = k.shape[1:]
-    _same_device(cache.device, k, v, positions, cos_sin, slot_mapping, scales, q, q_out)
-    with torch.cuda.device(cache.device):
-        kp, ks = _heads(k, "k")
-        vp, vs = _heads(v, "v")
-        qp, qs, op, os_, n_q = None, 0, None, 0, 0
-        if q is not None:
-            if q_out is None:
-                q_out = _empty_for(q, stream)
-            qp, qs = _heads(q, "q")
-            op, os_ = _heads(q_out, "q_out")
-            n_q = q.shape[1]
-        _check(getattr(lib, entry)(
-            qp, qs, kp, ks, vp, vs, _dev(positions, "positions"), _dev(cos_sin, "cos_sin"), cos_sin.shape[0],
-            cos_sin.shape[1], int(bool(interleaved)), _dev(slot_mapping, "slot_mapping"), k.shape[0],
-            _dev(cache, "cache"), _dev(scales, "cache"), n_blocks, block_size, n_q, n_kv, d, op, os_,
-            _DTYPE[k.dtype], _stream(stream, cache.device)), entry)
+def _append_rope(entry: str, k, v, positions, cos_sin, slot_mapping, cache, second, n_blocks, n_kv, d, q, q_out,
+                 interleaved, block_size, stream):
+    n = _check_kv(k, v, slot_mapping)
+    if positions.dtype != torch.int64 or positions.shape != (n,):
+        raise ValueError("positions must be int64 [num_tokens]")
+    if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
+        raise ValueError("cos_sin must be float32 [max_positions, rot_dim] (rotary_table)")
+    kp, ks = _heads(k, n, n_kv, d, "k")
+    vp, vs = _heads(v, n, n_kv, d, "v")
+    index = cache.get_device()
+    qp, qs, op, os_, n_q = None, 0, None, 0, 0
+    if q is not None:
+        if q.dtype != k.dtype or q.dim() != 3:
+            raise ValueError("q must be [num_tokens, n_q_heads, head_dim] of k's dtype")
+        n_q = q.shape[1]
+        qp, qs = _heads(q, n, n_q, d, "q")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    _on_device(index, k, v, positions, cos_sin, slot_mapping, second, q, q_out)
+    if q is not None:
+        if q_out is None:
+            q_out = _empty_for(q, stream)
+        elif q_out.dtype != q.dtype:
+            raise ValueError("q_out must have q's dtype")
+        op, os_ = _heads(q_out, n, n_q, d, "q_out")
+    rows, rot = cos_sin.shape
+    _launch(entry, index, stream, qp, qs, kp, ks, vp, vs, _flat(positions, "positions"), _flat(cos_sin, "cos_sin"),
+            rows, rot, 1 if interleaved else 0, _flat(slot_mapping, "slot_mapping"), n, _flat(cache, "cache"),
+            _flat(second, "cache"), n_blocks, block_size, n_q, n_kv, d, op, os_, _DTYPE[k.dtype])
     return q_out
 
 
@@ -693,14 +724,12 @@ def paged_kv_append_rope(k, v, positions, cos_sin, slot_mapping, k_cache, v_cach
     ``q_out`` (a new tensor by default; ``q_out=q`` rotates in place), or None
     without ``q``."""
     num_blocks, n_kv, bs, d = k_cache.shape
-    if bs != block_size or tuple(v_cache.shape) != tuple(k_cache.shape):
+    if bs != block_size or v_cache.shape != k_cache.shape:
         raise ValueError("cache shapes disagree")
-    _check_new_tokens(k, v, slot_mapping, n_kv, d)
     if k_cache.dtype != k.dtype or v_cache.dtype != k.dtype:
         raise ValueError("the caches must have k's dtype")
-    _check_rope(k, positions, cos_sin, q, q_out)
     return _append_rope("paged_kv_append_rope", k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, num_blocks,
-                        q, q_out, interleaved, bs, stream)
+                        n_kv, d, q, q_out, interleaved, bs, stream)
 
 
 def fp8_cache(num_blocks: int, n_kv_heads: int, head_dim: int, device="cuda"):
@@ -710,12 +739,12 @@ def fp8_cache(num_blocks: int, n_kv_heads: int, head_dim: int, device="cuda"):
 
 
 def _fp8_shape(kv_cache, kv_scales, block_size: int):
-    if kv_cache.dtype != torch.float8_e4m3fn or kv_cache.dim() != 5 or kv_cache.shape[2] != 2:
+    if kv_cache.dtype != torch.float8_e4m3fn or kv_cache.dim() != 5:
         raise ValueError("kv_cache must be float8_e4m3fn [num_blocks, n_kv_heads, 2, 16, head_dim]")
-    num_blocks, n_kv, _, bs, d = kv_cache.shape
-    if bs != block_size:
-        raise ValueError("block size disagrees with kv_cache")
-    if kv_scales.dtype != torch.float32 or tuple(kv_scales.shape) != (num_blocks, n_kv, 2):
+    num_blocks, n_kv, two, bs, d = kv_cache.shape
+    if two != 2 or bs != block_size:
+        raise ValueError("kv_cache must be [num_blocks, n_kv_heads, 2, block_size, head_dim]")
+    if kv_scales.dtype != torch.float32 or kv_scales.shape != (num_blocks, n_kv, 2):
         raise ValueError("kv_scales must be float32 [num_blocks, n_kv_heads, 2]")
     return num_blocks, n_kv, d
 
@@ -725,17 +754,14 @@ def paged_kv_append_fp8(k, v, slot_mapping, kv_cache, kv_scales, block_size: int
     (in place): e4m3 codes with one power-of-two scale for each block, kv head
     and K or V, which grows with what is appended (its rules, and which tokens
     of a call have to be consecutive, in include/pagedkv.h)."""
-    lib = _load()
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
-    _check_new_tokens(k, v, slot_mapping, n_kv, d)
-    _same_device(kv_cache.device, k, v, slot_mapping, kv_scales)
-    with torch.cuda.device(kv_cache.device):
-        kp, ks = _heads(k, "k")
-        vp, vs = _heads(v, "v")
-        _check(lib.paged_kv_append_fp8(kp, ks, vp, vs, _DTYPE[k.dtype], _dev(slot_mapping, "slot_mapping"),
-                                       k.shape[0], _dev(kv_cache, "kv_cache"), _dev(kv_scales, "kv_scales"),
-                                       num_blocks, block_size, n_kv, d, _stream(stream, kv_cache.device)),
-               "paged_kv_append_fp8")
+    n = _check_kv(k, v, slot_mapping)
+    kp, ks = _heads(k, n, n_kv, d, "k")
+    vp, vs = _heads(v, n, n_kv, d, "v")
+    index = kv_cache.get_device()
+    _on_device(index, k, v, slot_mapping, kv_scales)
+    _launch("paged_kv_append_fp8", index, stream, kp, ks, vp, vs, _DTYPE[k.dtype], _flat(slot_mapping, "slot_mapping"),
+            n, _flat(kv_cache, "kv_cache"), _flat(kv_scales, "kv_scales"), num_blocks, block_size, n_kv, d)
 
 
 def paged_kv_append_rope_fp8(k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales, q=None, q_out=None,
@@ -743,27 +769,22 @@ def paged_kv_append_rope_fp8(k, v, positions, cos_sin, slot_mapping, kv_cache, k
     """paged_kv_append_rope into the FP8 cache (keys are quantised from their
     fp32 rotation); returns the rotated queries as there."""
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
-    _check_new_tokens(k, v, slot_mapping, n_kv, d)
-    _check_rope(k, positions, cos_sin, q, q_out)
     return _append_rope("paged_kv_append_rope_fp8", k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales,
-                        num_blocks, q, q_out, interleaved, block_size, stream)
+                        num_blocks, n_kv, d, q, q_out, interleaved, block_size, stream)
 
 
 def paged_kv_copy_blocks_fp8(kv_cache, kv_scales, src_blocks, dst_blocks, block_size: int = 16, stream=None) -> None:
     """paged_kv_copy_blocks for the FP8 cache: codes and scales of whole blocks."""
-    lib = _load()
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
     if src_blocks.dtype != torch.int32 or dst_blocks.dtype != torch.int32 or src_blocks.shape != dst_blocks.shape:
         raise ValueError("src_blocks and dst_blocks must be int32 of one shape")
     n = src_blocks.numel()
     if n == 0:
         return
-    _same_device(kv_cache.device, kv_scales, src_blocks, dst_blocks)
-    with torch.cuda.device(kv_cache.device):
-        _check(lib.paged_kv_copy_blocks_fp8(_dev(kv_cache, "kv_cache"), _dev(kv_scales, "kv_scales"),
-                                            _dev(src_blocks, "src_blocks"), _dev(dst_blocks, "dst_blocks"), n,
-                                            num_blocks, block_size, n_kv, d, _stream(stream, kv_cache.device)),
-               "paged_kv_copy_blocks_fp8")
+    index = kv_cache.get_device()
+    _on_device(index, kv_scales, src_blocks, dst_blocks)
+    _launch("paged_kv_copy_blocks_fp8", index, stream, _flat(kv_cache, "kv_cache"), _flat(kv_scales, "kv_scales"),
+            _flat(src_blocks, "src_blocks"), _flat(dst_blocks, "dst_blocks"), n, num_blocks, block_size, n_kv, d)
 
 
 def paged_attention_fp8_workspace_size(batch: int, q_len: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
@@ -782,27 +803,31 @@ def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_len
     its context up to position ``ctx - q_len + i``), float16 or bfloat16.
     ``workspace``: :func:`new_workspace` of paged_attention_fp8_workspace_size
     bytes, for one call at a time.  Returns ``out`` (shape and dtype of q)."""
-    lib = _load()
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
-    if q.dim() not in (3, 4) or q.shape[-1] != d or q.dtype not in _DTYPE:
-        raise ValueError("q must be [batch, n_q, d] or [batch, q_len, n_q, d] with the cache's head_dim")
-    B, q_len, n_q = (q.shape[0], 1, q.shape[1]) if q.dim() == 3 else tuple(q.shape[:3])
+    shape = q.shape
+    if len(shape) == 3:
+        (B, n_q, qd), q_len = shape, 1
+    elif len(shape) == 4:
+        B, q_len, n_q, qd = shape
+    else:
+        raise ValueError("q must be [batch, n_q, d] or [batch, q_len, n_q, d]")
+    if qd != d or q.dtype not in _DTYPE:
+        raise ValueError("q must be float16 or bfloat16 with the cache's head_dim")
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise ValueError("block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or tuple(context_lens.shape) != (B,):
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("block_tables must be [batch, max_blocks_per_seq] and context_lens [batch]")
+    if out is not None and (out.dtype != q.dtype or out.shape != shape or not out.is_contiguous()):
+        raise ValueError("out must be a contiguous tensor of q's dtype and shape")
+    index = q.get_device()
+    _on_device(index, kv_cache, kv_scales, out, block_tables, context_lens, workspace)
     if out is None:
         out = _empty_for(q, stream)
-    if out.dtype != q.dtype or tuple(out.shape) != tuple(q.shape) or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor of q's dtype and shape")
-    _same_device(q.device, kv_cache, kv_scales, out, block_tables, context_lens, workspace)
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
-        ws_ptr, ws_bytes = _dev(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    with torch.cuda.device(q.device):
-        _check(lib.paged_attention_decode_fp8(
-            _dev(q, "q"), _dev(kv_cache, "kv_cache"), _dev(kv_scales, "kv_scales"),
-            _dev(block_tables, "block_tables"), block_tables.shape[1], _dev(context_lens, "context_lens"), B, q_len,
-            num_blocks, float(scale), n_q, n_kv, d, block_size, _dev(out, "out"), _DTYPE[q.dtype], ws_ptr, ws_bytes,
-            _stream(stream, q.device)), "paged_attention_decode_fp8")
+        ws_ptr, ws_bytes = _flat(workspace, "workspace"), workspace.numel() * workspace.element_size()
+    _launch("paged_attention_decode_fp8", index, stream, _flat(q, "q"), _flat(kv_cache, "kv_cache"),
+            _flat(kv_scales, "kv_scales"), _flat(block_tables, "block_tables"), block_tables.shape[1],
+            _flat(context_lens, "context_lens"), B, q_len, num_blocks, scale, n_q, n_kv, d, block_size, out.data_ptr(),
+            _DTYPE[q.dtype], ws_ptr, ws_bytes)
     return out
