@@ -64,10 +64,13 @@ int rope_heads_per_thread(int64_t columns, int heads, int sm_count) {
 
 template <int DT>
 pkv_status launch_append_f8(const AppendF8Params& p, unsigned grid, cudaStream_t s) {
+  const bool rope = p.rp.rope.rot > 0;
   if (p.rp.head_dim == 64)
-    pkv_append_f8_kernel<DT, 64><<<grid, 256, 0, s>>>(p);
+    rope ? pkv_append_f8_kernel<DT, 64, true><<<grid, 256, 0, s>>>(p)
+         : pkv_append_f8_kernel<DT, 64, false><<<grid, 256, 0, s>>>(p);
   else
-    pkv_append_f8_kernel<DT, 128><<<grid, 256, 0, s>>>(p);
+    rope ? pkv_append_f8_kernel<DT, 128, true><<<grid, 256, 0, s>>>(p)
+         : pkv_append_f8_kernel<DT, 128, false><<<grid, 256, 0, s>>>(p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -83,13 +86,13 @@ pkv_status append_f8(const RopeAppendParams& rp, pkv_dtype dtype, uint8_t* kv_ca
   p.rp = rp;
   p.kv = kv_cache;
   p.scales = kv_scales;
-  const int64_t heads2 = 2 * static_cast<int64_t>(rp.n_kv);
-  // A token a warp while all of them fit the device at once (a decode step:
-  // every token its own run); else 16, so that a prompt's warps are not
+  // A token a pair of warps while all of them fit the device at once (a decode
+  // step: every token its own run); else 16, so that a prompt's warps are not
   // mostly ones without a run start.
-  p.tokens_per_warp = rp.num_tokens * heads2 <= static_cast<int64_t>(di.sm_count) * 64 ? 1 : 16;
-  p.token_chunks = (rp.num_tokens + p.tokens_per_warp - 1) / p.tokens_per_warp;
-  const int64_t kv_ctas = (p.token_chunks * heads2 + 7) / 8;
+  p.tokens_per_pair = static_cast<int64_t>(rp.num_tokens) * rp.n_kv <= static_cast<int64_t>(di.sm_count) * 16 ? 1 : 16;
+  p.token_chunks = (rp.num_tokens + p.tokens_per_pair - 1) / p.tokens_per_pair;
+  const int64_t items = static_cast<int64_t>(p.token_chunks) * rp.n_kv * (p.tokens_per_pair == 1 ? 2 : 1);
+  const int64_t kv_ctas = (items + 3) / 4;
   const int64_t columns = static_cast<int64_t>(rp.num_tokens) * (rp.head_dim / 16);
   int64_t groups = 0;
   p.q_ctas = static_cast<int32_t>((columns + 255) / 256);

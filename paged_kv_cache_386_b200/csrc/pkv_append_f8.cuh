@@ -73,6 +73,22 @@ __device__ __forceinline__ void chunk_dims(int c, bool rotate, const RopeTable& 
   i1 = split ? t.rot / 2 + c * 8 : c * 16 + 8;
 }
 
+// Two fp32 values in a register pair: both products at once, each rounded as the
+// scalar product is.
+__device__ __forceinline__ uint64_t pack_f2(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpack_f2(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // cos and sin of the chunk's eight pairs.
 __device__ __forceinline__ void load_cos_sin(const RopeTable& t, int64_t pos, int c, float (&cs)[8], float (&sn)[8]) {
   const float* row = t.table + pos * t.rot + c * 8;
@@ -102,7 +118,22 @@ __device__ __forceinline__ void rotate_chunk(float (&x0)[8], float (&x1)[8], con
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) rotate_pair(x0[i], x1[i], cs[i], sn[i]);
+    for (int i = 0; i < 8; i += 2) {
+      // The sums stay scalar: packed products and packed sums were joined
+      // into fused multiply-adds.
+      const uint64_t a = pack_f2(x0[i], x0[i + 1]), b = pack_f2(x1[i], x1[i + 1]);
+      const uint64_t c = pack_f2(cs[i], cs[i + 1]), s = pack_f2(sn[i], sn[i + 1]);
+      float ac[2], bs[2], bc[2], as[2];
+      unpack_f2(mul_f2(a, c), ac[0], ac[1]);
+      unpack_f2(mul_f2(b, s), bs[0], bs[1]);
+      unpack_f2(mul_f2(b, c), bc[0], bc[1]);
+      unpack_f2(mul_f2(a, s), as[0], as[1]);
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        x0[i + k] = __fsub_rn(ac[k], bs[k]);
+        x1[i + k] = __fadd_rn(bc[k], as[k]);
+      }
+    }
   }
 }
 
@@ -133,7 +164,7 @@ template <int DT>
 __device__ __forceinline__ void rope_append_item(const RopeAppendParams& p, uint32_t item, int head_group,
                                                  int n_heads) {
   constexpr int kBytes = DTypeInfo<DT>::kBytes;
-  constexpr int kU = DT == kF32 ? 2 : 4;
+  constexpr int kU = 2;
   const uint32_t chunks = static_cast<uint32_t>(p.head_dim) / 16u;  // item = token * chunks + c
   if (item >= static_cast<uint32_t>(p.num_tokens) * chunks) return;
   const int64_t tok = item / chunks;
@@ -203,7 +234,7 @@ __device__ __forceinline__ void rope_append_item(const RopeAppendParams& p, uint
 }
 
 template <int DT>
-__global__ void __launch_bounds__(256) pkv_append_rope_kernel(const RopeAppendParams p) {
+__global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_rope_kernel(const RopeAppendParams p) {
   rope_append_item<DT>(p, blockIdx.x * 256u + threadIdx.x, blockIdx.y, p.n_q + 2 * p.n_kv);
 }
 
@@ -257,28 +288,63 @@ struct AppendF8Params {
   RopeAppendParams rp;  // inputs, strides, rotation (rope.rot = 0: none) and the query part
   uint8_t* kv;
   float* scales;
-  int32_t tokens_per_warp;  // 1 or 16 tokens whose runs a warp starts
-  int32_t token_chunks;     // ceil(num_tokens / tokens_per_warp)
+  int32_t tokens_per_pair;  // 1 or 16 tokens whose runs a pair of warps starts
+  int32_t token_chunks;     // ceil(num_tokens / tokens_per_pair)
   int32_t kv_ctas;          // CTAs of the K/V part; later CTAs rotate queries,
   int32_t q_ctas;           // this many for each group of heads_per_thread heads
 };
 
-// Consecutive tokens of the call in the same block are a run; a warp takes a
-// whole run of one kv head, for K or for V, so that the block's scale is
-// decided in one place: no atomics, and the result does not depend on
-// scheduling.  Of two tokens with the same slot in a run the last counts.
+// Magnitudes of two packed 16-bit values and the larger of each (NaN is passed over).
+template <bool kBf16>
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t w) {
+  uint32_t r;
+  w &= 0x7fff7fffu;
+  if constexpr (kBf16)
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w));
+  else
+    asm("max.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(w));
+  return r;
+}
+
+// The larger of two warps' maxima, the same in all their lanes.  `buf` takes turns
+// (0, 1), so that a value stays until both have read it.
+__device__ __forceinline__ float pair_max(float a, float (*exchange)[8], int buf, int warp) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+  if ((threadIdx.x & 31) == 0) exchange[buf][warp] = a;
+  named_bar_sync(1 + (warp >> 1), 64);
+  return fmaxf(a, exchange[buf][warp ^ 1]);
+}
+
+// Consecutive tokens of the call in the same block are a run; two warps take a
+// whole run of one kv head, K and then V (a step's single tokens: either), a half of the block's rows each,
+// so that the block's scale is decided in one place: no atomics, and the
+// result does not depend on scheduling.  Of two tokens with the same slot in a
+// run the last counts.
+//
+// D / 16 lanes hold a row, all rows of the half at once as loaded (16 registers
+// for 16-bit data); the maximum and the codes each widen (and rotate) them, so
+// that four CTAs fit an SM.  What bounds a prompt is how many rows are under
+// way.
 template <int DT, int D>
-__device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t blk, int64_t first, int head, bool is_v,
-                                              int lane) {
+struct F8Rows {
+  static constexpr int kLanes = D / 16;      // lanes of one head row, 16 dims each
+  static constexpr int kRows = 32 / kLanes;  // rows at a time
+  static constexpr int kIter = kBlockTokens / 2 / kRows;
+  Piece8<DT> x[kIter], y[kIter];
+};
+
+template <int DT, int D, bool kRope>
+__device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t blk, int first, int head,
+                                              int lane, int warp, float (*exchange)[8], int& buf,
+                                              int kind_begin, int kind_end) {
   constexpr int kBytes = DTypeInfo<DT>::kBytes;
-  constexpr int kLanes = D / 16;           // lanes of one head row, 16 dims each
-  constexpr int kRows = 32 / kLanes;       // rows at a time
-  constexpr int kIter = kBlockTokens / kRows;
+  constexpr int kLanes = F8Rows<DT, D>::kLanes, kRows = F8Rows<DT, D>::kRows, kIter = F8Rows<DT, D>::kIter;
+  const int row0 = (warp & 1) * (kBlockTokens / 2) + lane / kLanes;
   const RopeAppendParams& rp = p.rp;
-  const bool has_rope = rp.rope.rot > 0;
   // Token of the call for each offset of the block (lane = offset), -1 none.
-  int64_t src = -1;
-  for (int64_t base = first;; base += 32) {
+  int src = -1;
+  for (int base = first;; base += 32) {
     int64_t s = -1;
     if (base + lane < rp.num_tokens) s = __ldg(rp.slot_mapping + base + lane);
     const uint32_t other = __ballot_sync(0xffffffffu, s < 0 || (s >> 4) != blk);
@@ -286,7 +352,7 @@ __device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t b
     int off = -1;
     if (lane < n) {
       off = static_cast<int>(s & 15);
-      if (has_rope) {
+      if constexpr (kRope) {
         const int64_t pos = __ldg(rp.rope.positions + base + lane);
         if (pos < 0 || pos >= rp.rope.max_pos) {  // left out, as if it were padding
           flag_error(PKV_DEVERR_POSITION);
@@ -294,106 +360,160 @@ __device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t b
         }
       }
     }
-#pragma unroll
-    for (int j = 0; j < kBlockTokens; ++j) {
-      const uint32_t at = __ballot_sync(0xffffffffu, off == j);
-      if (lane == j && at) src = base + 31 - __clz(at);
+    const int off0 = __shfl_sync(0xffffffffu, off, 0);
+    if (__all_sync(0xffffffffu, lane >= n || (off0 >= 0 && off == off0 + lane))) {  // in order, as prompts and steps are
+      if (lane >= off0 && lane < off0 + n) src = base + lane - off0;
+    } else {
+#pragma unroll 1
+      for (int j = 0; j < kBlockTokens; ++j) {
+        const uint32_t at = __ballot_sync(0xffffffffu, off == j);
+        if (lane == j && at) src = base + 31 - __clz(at);
+      }
     }
     if (n < 32) break;
   }
   if (!__any_sync(0xffffffffu, src >= 0)) return;
   const bool fresh = __shfl_sync(0xffffffffu, src, 0) >= 0;
 
-  float* scale_at = p.scales + (blk * rp.n_kv + head) * 2 + (is_v ? 1 : 0);
-  const float s_old = *scale_at;
-  const int c = lane % kLanes;
-  const bool rotate = has_rope && !is_v;
-  int i0, i1;
-  chunk_dims(c, rotate, rp.rope, i0, i1);
-  const uint8_t* base = (is_v ? rp.v : rp.k) + static_cast<int64_t>(head) * D * kBytes;
-  const int64_t stride = is_v ? rp.v_stride : rp.k_stride;
-  Piece8<DT> x[kIter], y[kIter];
-  int64_t tok[kIter];
+#pragma unroll 1
+  for (int kind = kind_begin; kind < kind_end; ++kind) {
+    const bool is_v = kind == 1;
+    F8Rows<DT, D> r;
+    const int c = lane % kLanes;
+    const bool rotate = kRope && !is_v;
+    const bool turns = rotate && c * 16 < rp.rope.rot;
+    int i0, i1;
+    chunk_dims(c, rotate, rp.rope, i0, i1);
+    const int64_t block_head = blk * rp.n_kv + head;
+    float* scale_at = p.scales + block_head * 2 + (is_v ? 1 : 0);
+    const float s_old = *scale_at;
+    const uint8_t* base = (is_v ? rp.v : rp.k) + static_cast<int64_t>(head) * D * kBytes;
+    const int64_t stride = is_v ? rp.v_stride : rp.k_stride;
+    int tok[kIter];
 #pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    tok[it] = __shfl_sync(0xffffffffu, src, it * kRows + lane / kLanes);
-    x[it].a = x[it].b = y[it].a = y[it].b = make_uint4(0u, 0u, 0u, 0u);
-    if (tok[it] < 0) continue;
-    x[it].load(base + tok[it] * stride + i0 * kBytes);
-    y[it].load(base + tok[it] * stride + i1 * kBytes);
-  }
-  float v0[kIter][8], v1[kIter][8];
-  float amax = 0.f;
-#pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    x[it].widen(v0[it]);
-    y[it].widen(v1[it]);
-    if (rotate && c * 16 < rp.rope.rot && tok[it] >= 0) {
-      float cs[8], sn[8];
-      load_cos_sin(rp.rope, __ldg(rp.rope.positions + tok[it]), c, cs, sn);
-      rotate_chunk(v0[it], v1[it], cs, sn, rp.rope.interleaved != 0);
+    for (int it = 0; it < kIter; ++it) {
+      tok[it] = __shfl_sync(0xffffffffu, src, row0 + it * kRows);
+      r.x[it].a = r.x[it].b = r.y[it].a = r.y[it].b = make_uint4(0u, 0u, 0u, 0u);
+      if (tok[it] < 0) continue;
+      r.x[it].load(base + tok[it] * stride + i0 * kBytes);
+      r.y[it].load(base + tok[it] * stride + i1 * kBytes);
     }
-    // Infinities and NaN do not set the scale.
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a = fabsf(v0[it][i]), b = fabsf(v1[it][i]);
-      if (a <= 3.402823466e38f) amax = fmaxf(amax, a);
-      if (b <= 3.402823466e38f) amax = fmaxf(amax, b);
-    }
-  }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float need = f8_scale_for(amax);
-  const float s_new = fresh ? need : fmaxf(s_old, need);
-  const float inv = 1.0f / s_new;  // exact: a power of two
-  uint8_t* tile = p.kv + (static_cast<int64_t>(blk) * rp.n_kv + head) * f8_tile_bytes(D) + (is_v ? kBlockTokens * D : 0);
-  const bool regrid = !fresh && s_new != s_old;
-  const float ratio = s_old * inv;
-#pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    uint8_t* row = tile + (it * kRows + lane / kLanes) * D;
-    if (tok[it] >= 0) {
-      uint32_t w[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        w[i] = f8_pack2(v0[it][4 * i] * inv, v0[it][4 * i + 1] * inv) |
-               (f8_pack2(v0[it][4 * i + 2] * inv, v0[it][4 * i + 3] * inv) << 16);
-        w[2 + i] = f8_pack2(v1[it][4 * i] * inv, v1[it][4 * i + 1] * inv) |
-                   (f8_pack2(v1[it][4 * i + 2] * inv, v1[it][4 * i + 3] * inv) << 16);
+    // Row `it` as fp32, rotated.
+    auto values = [&](int it, float (&a)[8], float (&b)[8]) {
+      r.x[it].widen(a);
+      r.y[it].widen(b);
+      if constexpr (kRope) {
+        if (turns && tok[it] >= 0) {
+          float cs[8], sn[8];
+          load_cos_sin(rp.rope, __ldg(rp.rope.positions + tok[it]), c, cs, sn);
+          rotate_chunk(a, b, cs, sn, rp.rope.interleaved != 0);
+        }
       }
-      *reinterpret_cast<uint2*>(row + i0) = make_uint2(w[0], w[1]);
-      *reinterpret_cast<uint2*>(row + i1) = make_uint2(w[2], w[3]);
-    } else if (fresh) {
-      *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-    } else if (regrid) {
-      uint4* at = reinterpret_cast<uint4*>(row + c * 16);
-      *at = f8_rescale(*at, ratio);
+    };
+    float amax = 0.f;
+    if (DT != kF32 && !rotate) {
+      uint32_t m2 = 0u;
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        const uint32_t w[8] = {r.x[it].a.x, r.x[it].a.y, r.x[it].a.z, r.x[it].a.w,
+                               r.y[it].a.x, r.y[it].a.y, r.y[it].a.z, r.y[it].a.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m2 = max_abs2<DT == kBF16>(m2, w[i]);
+      }
+      float lo, hi;
+      unpack2<DT == kBF16>(m2, lo, hi);
+      amax = fmaxf(lo, hi);
+    } else {
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        float a[8], b[8];
+        values(it, a, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(a[i]), fabsf(b[i])));
+      }
     }
+    amax = pair_max(amax, exchange, buf, warp);
+    buf ^= 1;
+    if (amax > 3.402823466e38f) {  // an infinity does not set the scale
+      amax = 0.f;
+#pragma unroll
+      for (int it = 0; it < kIter; ++it) {
+        float a[8], b[8];
+        values(it, a, b);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          if (fabsf(a[i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(a[i]));
+          if (fabsf(b[i]) <= 3.402823466e38f) amax = fmaxf(amax, fabsf(b[i]));
+        }
+      }
+      amax = pair_max(amax, exchange, buf, warp);
+      buf ^= 1;
+    }
+    const float need = f8_scale_for(amax);
+    const float s_new = fresh ? need : fmaxf(s_old, need);
+    const float inv = 1.0f / s_new;  // exact: a power of two
+    uint8_t* tile = p.kv + block_head * f8_tile_bytes(D) + (is_v ? kBlockTokens * D : 0);
+    const bool regrid = !fresh && s_new != s_old;
+#pragma unroll
+    for (int it = 0; it < kIter; ++it) {
+      uint8_t* row = tile + (row0 + it * kRows) * D;
+      if (tok[it] >= 0) {
+        float a[8], b[8];
+        values(it, a, b);
+        uint32_t w[4];
+        const uint64_t inv2 = pack_f2(inv, inv);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          float v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = i < 2 ? a[4 * i + k] : b[4 * (i - 2) + k];
+          unpack_f2(mul_f2(pack_f2(v[0], v[1]), inv2), v[0], v[1]);
+          unpack_f2(mul_f2(pack_f2(v[2], v[3]), inv2), v[2], v[3]);
+          w[i] = f8_pack2(v[0], v[1]) | (f8_pack2(v[2], v[3]) << 16);
+        }
+        if (rotate) {
+          *reinterpret_cast<uint2*>(row + i0) = make_uint2(w[0], w[1]);
+          *reinterpret_cast<uint2*>(row + i1) = make_uint2(w[2], w[3]);
+        } else {
+          *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      } else if (fresh) {
+        *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+      } else if (regrid) {
+        uint4* at = reinterpret_cast<uint4*>(row + c * 16);
+        *at = f8_rescale(*at, s_old * inv);
+      }
+    }
+    // (The other warp has read the old scale: in front of the exchange.)
+    if (lane == 0 && (warp & 1) == 0 && (fresh || regrid)) *scale_at = s_new;
   }
-  if (lane == 0 && (fresh || regrid)) *scale_at = s_new;
 }
 
-template <int DT, int D>
-__global__ void __launch_bounds__(256) pkv_append_f8_kernel(const AppendF8Params p) {
+template <int DT, int D, bool kRope>
+__global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_f8_kernel(const AppendF8Params p) {
   const RopeAppendParams& rp = p.rp;
-  if (static_cast<int>(blockIdx.x) >= p.kv_ctas) {  // queries
+  if (kRope && static_cast<int>(blockIdx.x) >= p.kv_ctas) {  // queries
     const uint32_t i = blockIdx.x - p.kv_ctas;
     rope_append_item<DT>(rp, (i % p.q_ctas) * 256u + threadIdx.x, i / p.q_ctas, rp.n_q);
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5);
-  const int heads2 = 2 * rp.n_kv;
-  const int64_t chunk = w / heads2;
+  __shared__ float exchange[2][8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int buf = 0;
+  const int64_t w = static_cast<int64_t>(blockIdx.x) * (blockDim.x >> 6) + (warp >> 1);
+  const bool one_kind = p.tokens_per_pair == 1;  // K and V to a pair each
+  const int items = one_kind ? 2 * rp.n_kv : rp.n_kv;
+  const int64_t chunk = w / items;
   if (chunk >= p.token_chunks) return;
-  const int h2 = static_cast<int>(w % heads2);
+  const int item = static_cast<int>(w % items), head = one_kind ? item >> 1 : item;
+  const int kind_begin = one_kind ? item & 1 : 0, kind_end = one_kind ? kind_begin + 1 : 2;
   // Lane l looks at token l - 1 of the chunk, so that lane 0 holds the token before it.
-  const int64_t t = chunk * p.tokens_per_warp + lane - 1;
+  const int64_t t = chunk * p.tokens_per_pair + lane - 1;
   int64_t blk = -1;
-  if (t >= 0 && t < rp.num_tokens && lane <= p.tokens_per_warp) {
+  if (t >= 0 && t < rp.num_tokens && lane <= p.tokens_per_pair) {
     const int64_t s = __ldg(rp.slot_mapping + t);
     if (s >= rp.num_slots) {
-      if (h2 == 0 && lane > 0) flag_error(PKV_DEVERR_SLOT);
+      if (item == 0 && lane > 0) flag_error(PKV_DEVERR_SLOT);
     } else if (s >= 0) {
       blk = s >> 4;
     }
@@ -403,7 +523,8 @@ __global__ void __launch_bounds__(256) pkv_append_f8_kernel(const AppendF8Params
   while (starts) {
     const int l = __ffs(starts) - 1;
     starts &= starts - 1;
-    append_f8_run<DT, D>(p, __shfl_sync(0xffffffffu, blk, l), chunk * p.tokens_per_warp + l - 1, h2 >> 1, h2 & 1, lane);
+    append_f8_run<DT, D, kRope>(p, __shfl_sync(0xffffffffu, blk, l), static_cast<int>(chunk * p.tokens_per_pair) + l - 1,
+                                head, lane, warp, exchange, buf, kind_begin, kind_end);
   }
 }
 
