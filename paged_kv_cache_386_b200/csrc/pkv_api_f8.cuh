@@ -288,7 +288,7 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
   p.total_rows = p.group * q_len;
   decode_f8_segments(p.total_rows, &p.nseg, &p.rows);
   p.ng = n_kv_heads * p.nseg;
-  if (static_cast<int64_t>(batch) * (max_blocks_per_seq + kF8SegSlots) * p.ng > INT32_MAX) return PKV_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(batch) * (max_blocks_per_seq + f8_seg_slots(2)) * p.ng > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   p.rec_floats = p.rows * (head_dim + 4);
   p.scale_log2 = scale * 1.4426950408889634f;
   p.wait_limit_ns = kWaitLimitNs;

@@ -39,7 +39,10 @@ namespace pkv {
 
 constexpr int kF8MaxStages = 6;                       // ring slots of a warp
 constexpr int kF8MinSlots = 2;                        // slots that make a unit worth its merge
-constexpr int kF8SegSlots = 2;                        // a segment's fixed work, in tiles
+// A segment's fixed work, in tiles.  Measured with none: the slowest warp of 256
+// mixed lengths of 1 to 1300 tokens, 32/32 heads, ended 25% after the mean (263 us,
+// 216 with two); with 16 rows, seven against two: 46.4 -> 42.8 us (32 x 4 queries).
+__host__ __device__ constexpr int f8_seg_slots(int NR) { return NR == 1 ? 2 : 7; }
 constexpr int kF8W1 = 16, kF8W2 = 8;                  // warps of a CTA with up to 8 rows, with 16
 constexpr int kF8HeaderBytes = 4096;                  // workspace: a counter per CTA
 constexpr float kF8RefBelow = 7.f, kF8RefSlack = 14.f;
@@ -481,26 +484,32 @@ __device__ __noinline__ void f8_merge(const DecodeF8Params& p, const F8Pieces pc
     float mj[kBatch], lj[kBatch], o[kBatch][DL];
 #pragma unroll
     for (int jj = 0; jj < kBatch; ++jj) {
-      const int j = min(j0 + jj * kStep, pc.n - 1);  // no branch between loads; a repeated piece gets no weight
+      const int j = j0 + jj * kStep;  // predicated loads: no branch between them
+      const int is = j < pc.n;
       const float* r = at + (j == 0 ? pc.first : j == pc.n - 1 && pc.last != nullptr ? pc.last : pc.base + j * static_cast<int64_t>(pc.stride));
-      asm volatile("ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];" : "=f"(mj[jj]), "=f"(lj[jj]) : "l"(r + D));
+      mj[jj] = -INFINITY;
+      lj[jj] = 0.f;
+      asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %3, 0;\n @p ld.relaxed.gpu.v2.f32 {%0, %1}, [%2];\n}"
+                   : "+f"(mj[jj]), "+f"(lj[jj])
+                   : "l"(r + D), "r"(is));
 #pragma unroll
-      for (int i = 0; i < DL; i += 4)
-        asm volatile("ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];"
-                     : "=f"(o[jj][i]), "=f"(o[jj][i + 1]), "=f"(o[jj][i + 2]), "=f"(o[jj][i + 3])
-                     : "l"(r + dim + i));
+      for (int i = 0; i < DL; i += 4) {
+        o[jj][i] = o[jj][i + 1] = o[jj][i + 2] = o[jj][i + 3] = 0.f;
+        asm volatile("{\n .reg .pred p;\n setp.ne.s32 p, %5, 0;\n @p ld.relaxed.gpu.v4.f32 {%0, %1, %2, %3}, [%4];\n}"
+                     : "+f"(o[jj][i]), "+f"(o[jj][i + 1]), "+f"(o[jj][i + 2]), "+f"(o[jj][i + 3])
+                     : "l"(r + dim + i), "r"(is));
+      }
     }
     // -inf: no token seen so far; those pieces' sums are 0 (or NaN, which stays).
     float Mb = M;
 #pragma unroll
-    for (int jj = 0; jj < kBatch; ++jj) Mb = fmaxf(Mb, mj[jj]);  // (a repeated one changes nothing here)
+    for (int jj = 0; jj < kBatch; ++jj) Mb = fmaxf(Mb, mj[jj]);
     const float alpha = M == -INFINITY ? 1.f : exp2f(M - Mb);
     L *= alpha;
 #pragma unroll
     for (int i = 0; i < DL; ++i) acc[i] *= alpha;
 #pragma unroll
     for (int jj = 0; jj < kBatch; ++jj) {
-      if (j0 + jj * kStep >= pc.n) continue;
       const float w = mj[jj] == -INFINITY ? 1.f : exp2f(mj[jj] - Mb);
       L = fmaf(w, lj[jj], L);
 #pragma unroll
@@ -540,7 +549,7 @@ __device__ __noinline__ void f8_merge(const DecodeF8Params& p, const F8Pieces pc
                                                     pack2<kBf16>(acc[i + 2] * inv, acc[i + 3] * inv));
 }
 
-// Work is counted in slots: a segment has kF8SegSlots for its start and end (Q,
+// Work is counted in slots: a segment has f8_seg_slots for its start and end (Q,
 // the first maxima, the output), then one for each tile.  A unit's range of
 // slots begins at its share of them, or at the segment's first slot where that
 // share begins before the segment's second tile.
@@ -551,6 +560,7 @@ struct F8Walk {
 };
 
 // The segment of slot k.
+template <int kSeg>
 __device__ __forceinline__ F8Walk f8_find(const int* prefix, const int* ctxs, int B, int k) {
   int lo = 0, hi = B;  // prefix[lo] <= k < prefix[hi]
   while (hi - lo > 1) {
@@ -561,14 +571,15 @@ __device__ __forceinline__ F8Walk f8_find(const int* prefix, const int* ctxs, in
   w.b = lo;
   w.nb = (ctxs[lo] + kBlockTokens - 1) / kBlockTokens;
   const int local = k - prefix[lo];
-  w.hg = local / (w.nb + kF8SegSlots);
-  w.st = k - local + w.hg * (w.nb + kF8SegSlots);
-  w.j = max(0, k - w.st - kF8SegSlots);
+  w.hg = local / (w.nb + kSeg);
+  w.st = k - local + w.hg * (w.nb + kSeg);
+  w.j = max(0, k - w.st - kSeg);
   return w;
 }
 
+template <int kSeg>
 __device__ __forceinline__ void f8_next_segment(F8Walk& w, const int* prefix, const int* ctxs, int B, int ng) {
-  w.st += w.nb + kF8SegSlots;
+  w.st += w.nb + kSeg;
   w.j = 0;
   if (++w.hg == ng) {
     w.hg = 0;
@@ -580,10 +591,11 @@ __device__ __forceinline__ void f8_next_segment(F8Walk& w, const int* prefix, co
 }
 
 // Where unit u's slots begin.
+template <int kSeg>
 __device__ __forceinline__ int f8_unit_begin(const Sched& sc, int u, const int* prefix, const int* ctxs, int B) {
   const int k = unit_begin(sc, u);
   if (u == 0 || u >= sc.U) return k;
-  const F8Walk w = f8_find(prefix, ctxs, B, k);
+  const F8Walk w = f8_find<kSeg>(prefix, ctxs, B, k);
   return w.j == 0 ? w.st : k;
 }
 
@@ -598,7 +610,7 @@ struct F8Group {
 // The CTA's segments with a share in several units or CTAs, in order: of the
 // candidates that one comes from before the CTA, and one starts in each unit and
 // goes on behind it.  By one warp, while the first copies are under way.
-template <int W>
+template <int W, int kSeg>
 __device__ __noinline__ void f8_find_groups(const DecodeF8Params& p, const Sched sc, int per_cta, int u0, int n_units,
                                             const int* bnd, const int* prefix, const int* ctxs, F8Group* groups,
                                             int* n_groups) {
@@ -608,18 +620,18 @@ __device__ __noinline__ void f8_find_groups(const DecodeF8Params& p, const Sched
   F8Group gr;
   if (lane <= n_units && A < E) {
     const int w = max(0, lane - 1), k = lane == 0 ? A : bnd[w + 1] - 1;
-    const F8Walk f = f8_find(prefix, ctxs, p.batch, k);
+    const F8Walk f = f8_find<kSeg>(prefix, ctxs, p.batch, k);
     gr.b = f.b;
     gr.hg = f.hg;
     gr.st = f.st;
-    gr.en = f.st + f.nb + kF8SegSlots;
+    gr.en = f.st + f.nb + kSeg;
     valid = lane == 0 ? gr.st < A : bnd[w] < bnd[w + 1] && gr.st >= bnd[w] && gr.en > bnd[w + 1];
     const int last = unit_of_tile(sc, gr.en - 1);
     gr.ua = w;
     gr.ub = min(last - u0, n_units - 1);
     if (lane == 0)  // units in front of the first tile have no piece
       while (bnd[gr.ua + 1] == A) ++gr.ua;
-    gr.c0 = unit_of_tile(sc, gr.st + kF8SegSlots) / per_cta;
+    gr.c0 = unit_of_tile(sc, gr.st + kSeg) / per_cta;
     gr.n_ctas = last / per_cta - gr.c0 + 1;
     gr.kvh = gr.hg / p.nseg;
     gr.first = (gr.hg - gr.kvh * p.nseg) * p.rows;
@@ -643,7 +655,7 @@ template <int D, int NR, bool kBf16>
 __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     pkv_decode_f8_kernel(const __grid_constant__ CUtensorMap tm, const __grid_constant__ DecodeF8Params p) {
   constexpr int kTile = f8_tile_bytes(D);
-  constexpr int W = f8_warps(NR), kThreads = W * 32;
+  constexpr int W = f8_warps(NR), kThreads = W * 32, kSeg = f8_seg_slots(NR);
   using Consumer = F8Consumer<D, NR, kBf16>;
 
   extern __shared__ uint8_t smem_raw[];
@@ -679,7 +691,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     const int per = (B + kThreads - 1) / kThreads;
     const int lo = min(B, static_cast<int>(threadIdx.x) * per), hi = min(B, lo + per);
     const int max_ctx = p.max_blocks_per_seq * kBlockTokens;
-    auto slots_of = [&](int c) { return c > 0 ? ((c + kBlockTokens - 1) / kBlockTokens + kF8SegSlots) * p.ng : 0; };
+    auto slots_of = [&](int c) { return c > 0 ? ((c + kBlockTokens - 1) / kBlockTokens + kSeg) * p.ng : 0; };
     int local = 0;
     for (int b = lo; b < hi; ++b) {
       const int c0 = __ldg(p.context_lens + b);
@@ -722,7 +734,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   const int per_cta = (sc.U + gridDim.x - 1) / static_cast<int>(gridDim.x);
   const int u0 = blockIdx.x * per_cta, n_units = min(sc.U - u0, per_cta);  // this CTA's units
   if (T == 0 || n_units <= 0) return;
-  if (threadIdx.x <= n_units) bnd[lane] = f8_unit_begin(sc, u0 + lane, prefix, ctxs, B);
+  if (threadIdx.x <= n_units) bnd[lane] = f8_unit_begin<kSeg>(sc, u0 + lane, prefix, ctxs, B);
   __syncthreads();
 
   // Rows of segment hg of a sequence: kv head, first of its rows, how many.
@@ -746,14 +758,14 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
         cp_async_16(qbuf + i * 16, p.q + f8_row_at(p, b, kvh, first + i / kChunks, D) + (i % kChunks) * 8);
       cp_async_commit();
     };
-    F8Walk wk = f8_find(prefix, ctxs, B, k0);
+    F8Walk wk = f8_find<kSeg>(prefix, ctxs, B, k0);
     fetch_q(wk.b, wk.hg);  // in front of the copies that fill the memory's queues
 
     // Issue side: the warp copies its own tiles, a ring ahead of their use.
     // Block ids come in windows of 32 (lane i holds entry wj + i of sequence
     // wb's table); the window that is needed next is loaded when one is taken.
     F8Walk wi = wk;
-    int left = k1 - max(k0, wi.st + kF8SegSlots);  // slots from tile wi.j on; a tile while positive
+    int left = k1 - max(k0, wi.st + kSeg);  // slots from tile wi.j on; a tile while positive
     auto table = [&](int b, int j) {
       const int at = j + lane;
       return at < p.max_blocks_per_seq ? __ldg(p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq + at) : -1;
@@ -808,13 +820,13 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
         left -= k;
         wi.j += k;
         if (wi.j == wi.nb) {
-          f8_next_segment(wi, prefix, ctxs, B, p.ng);
-          left -= kF8SegSlots;
+          f8_next_segment<kSeg>(wi, prefix, ctxs, B, p.ng);
+          left -= kSeg;
         }
       }
     };
     issue(slot_begin, S);
-    if (warp == W - 1) f8_find_groups<W>(p, sc, per_cta, u0, n_units, bnd, prefix, ctxs, groups, &n_groups);
+    if (warp == W - 1) f8_find_groups<W, kSeg>(p, sc, per_cta, u0, n_units, bnd, prefix, ctxs, groups, &n_groups);
 
     Consumer cs;
     int slot = slot_begin;
@@ -824,9 +836,9 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     while (true) {
       int kvh, first;
       const int rows = seg_rows(wk.hg, kvh, first);
-      const int end = min(wk.nb, k1 - wk.st - kF8SegSlots), ctx = ctxs[wk.b];
+      const int end = min(wk.nb, k1 - wk.st - kSeg), ctx = ctxs[wk.b];
       F8Walk nx = wk;
-      f8_next_segment(nx, prefix, ctxs, B, p.ng);
+      f8_next_segment<kSeg>(nx, prefix, ctxs, B, p.ng);
       const bool more = nx.st < k1;
       cp_async_wait_all();
       __syncwarp();
@@ -886,7 +898,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
         }
       }
   } else if (warp == W - 1) {
-    f8_find_groups<W>(p, sc, per_cta, u0, n_units, bnd, prefix, ctxs, groups, &n_groups);
+    f8_find_groups<W, kSeg>(p, sc, per_cta, u0, n_units, bnd, prefix, ctxs, groups, &n_groups);
   }
   __syncthreads();
 
