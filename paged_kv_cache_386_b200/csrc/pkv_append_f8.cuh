@@ -450,133 +450,6 @@ __device__ __forceinline__ void append_f8_rows(const AppendF8Params& p, int64_t 
   if ((threadIdx.x & 31) == 0 && (warp & 1) == 0 && (fresh || regrid)) *scale_at = s_new;
 }
 
-// One kv head's K or V of a run: this lane's part of the rows tok[it] (token of
-// the call, -1: none) at block offsets row0 + it kRows.
-template <int DT, int D, bool kRotate>
-__device__ __forceinline__ void append_f8_rows(const AppendF8Params& p, int64_t blk, int head, bool is_v,
-                                               const int (&tok)[F8Rows<D>::kIter], int c, int row0, bool fresh, int warp,
-                                               float (*exchange)[8], int& buf) {
-  constexpr int kBytes = DTypeInfo<DT>::kBytes;
-  constexpr int kRows = F8Rows<D>::kRows, kIter = F8Rows<D>::kIter;
-  constexpr float kLargest = 3.402823466e38f;
-  const RopeAppendParams& rp = p.rp;
-  const int64_t block_head = blk * rp.n_kv + head;
-  float* scale_at = p.scales + block_head * 2 + (is_v ? 1 : 0);
-  const float s_old = *scale_at;
-  const uint8_t* base = (is_v ? rp.v : rp.k) + static_cast<int64_t>(head) * D * kBytes;
-  const int64_t stride = is_v ? rp.v_stride : rp.k_stride;
-  int i0, i1;
-  chunk_dims(c, kRotate, rp.rope, i0, i1);
-  // Not rotated, the rows stay as loaded and are widened where they are used;
-  // rotated ones are kept as fp32.
-  Piece8<DT> x[kIter], y[kIter];
-  float v0[kRotate ? kIter : 1][8], v1[kRotate ? kIter : 1][8];
-#pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    x[it].a = x[it].b = y[it].a = y[it].b = make_uint4(0u, 0u, 0u, 0u);
-    if (tok[it] < 0) continue;
-    x[it].load(base + tok[it] * stride + i0 * kBytes);
-    y[it].load(base + tok[it] * stride + i1 * kBytes);
-  }
-  if constexpr (kRotate) {
-#pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      x[it].widen(v0[it]);
-      y[it].widen(v1[it]);
-      if (c * 16 < rp.rope.rot && tok[it] >= 0) {
-        float cs[8], sn[8];
-        load_cos_sin(rp.rope, __ldg(rp.rope.positions + tok[it]), c, cs, sn);
-        rotate_chunk(v0[it], v1[it], cs, sn, rp.rope.interleaved != 0);
-      }
-    }
-  }
-  auto values = [&](int it, float (&a)[8], float (&b)[8]) {
-    if constexpr (kRotate) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) a[i] = v0[it][i], b[i] = v1[it][i];
-    } else {
-      x[it].widen(a);
-      y[it].widen(b);
-    }
-  };
-
-  float amax = 0.f;
-  if constexpr (DT != kF32 && !kRotate) {
-    uint32_t m2 = 0u;
-#pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      const uint32_t w[8] = {x[it].a.x, x[it].a.y, x[it].a.z, x[it].a.w, y[it].a.x, y[it].a.y, y[it].a.z, y[it].a.w};
-#pragma unroll
-      for (int i = 0; i < 8; ++i) m2 = max_abs2<DT == kBF16>(m2, w[i]);
-    }
-    float lo, hi;
-    unpack2<DT == kBF16>(m2, lo, hi);
-    amax = fmaxf(lo, hi);
-  } else {
-#pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      float a[8], b[8];
-      values(it, a, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fmaxf(fabsf(a[i]), fabsf(b[i])));
-    }
-  }
-  amax = pair_max(amax, exchange, buf, warp);
-  buf ^= 1;
-  if (amax > kLargest) {  // an infinity does not set the scale
-    amax = 0.f;
-#pragma unroll
-    for (int it = 0; it < kIter; ++it) {
-      float a[8], b[8];
-      values(it, a, b);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        if (fabsf(a[i]) <= kLargest) amax = fmaxf(amax, fabsf(a[i]));
-        if (fabsf(b[i]) <= kLargest) amax = fmaxf(amax, fabsf(b[i]));
-      }
-    }
-    amax = pair_max(amax, exchange, buf, warp);
-    buf ^= 1;
-  }
-  const float need = f8_scale_for(amax);
-  const float s_new = fresh ? need : fmaxf(s_old, need);
-  const float inv = 1.0f / s_new;  // exact: a power of two
-  uint8_t* tile = p.kv + block_head * f8_tile_bytes(D) + (is_v ? kBlockTokens * D : 0);
-  const bool regrid = !fresh && s_new != s_old;
-#pragma unroll
-  for (int it = 0; it < kIter; ++it) {
-    uint8_t* row = tile + (row0 + it * kRows) * D;
-    if (tok[it] >= 0) {
-      float a[8], b[8];
-      values(it, a, b);
-      uint32_t w[4];
-      const uint64_t inv2 = pack_f2(inv, inv);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float v[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = i < 2 ? a[4 * i + k] : b[4 * (i - 2) + k];
-        unpack_f2(mul_f2(pack_f2(v[0], v[1]), inv2), v[0], v[1]);
-        unpack_f2(mul_f2(pack_f2(v[2], v[3]), inv2), v[2], v[3]);
-        w[i] = f8_pack2(v[0], v[1]) | (f8_pack2(v[2], v[3]) << 16);
-      }
-      if constexpr (kRotate) {
-        *reinterpret_cast<uint2*>(row + i0) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2*>(row + i1) = make_uint2(w[2], w[3]);
-      } else {
-        *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-      }
-    } else if (fresh) {
-      *reinterpret_cast<uint4*>(row + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-    } else if (regrid) {
-      uint4* at = reinterpret_cast<uint4*>(row + c * 16);
-      *at = f8_rescale(*at, s_old * inv);
-    }
-  }
-  // (The other warp has read the old scale: in front of the exchange.)
-  if ((threadIdx.x & 31) == 0 && (warp & 1) == 0 && (fresh || regrid)) *scale_at = s_new;
-}
-
 // Consecutive tokens of the call in the same block are a run; two warps take a
 // whole run of one kv head, K and then V (a step's single tokens: either), a
 // half of the block's rows each, so that the block's scale is decided in one
