@@ -614,7 +614,15 @@ pkv_status paged_kv_copy_blocks_fp8(uint8_t* kv_cache, float* kv_scales, const i
  *   q, out    : device, [batch][q_len][n_q_heads][head_dim], f16 or bf16
  *   q_len     : 1 .. 16, the last tokens of every context; query i sees tokens
  *               j < context_lens[b] - q_len + i + 1
- *   workspace : paged_attention_fp8_workspace_size() bytes, or NULL
+ *   kv_scales : of the blocks read: positive and normal, as the appends write
+ *               them (any such value, not only powers of two)
+ *   workspace : paged_attention_fp8_workspace_size() bytes on the current
+ *               device, 256-byte aligned, zero-filled before its first use and
+ *               for one call at a time (each call leaves it ready for the
+ *               next, of any sizes that fit it); NULL allocates it on `stream`.
+ * A block id or a context length out of range is treated as in
+ * paged_attention_decode_mq.  A NaN in a key or value reaches the rows that see
+ * its token, and no others.
  */
 pkv_status paged_attention_fp8_workspace_size(int32_t batch, int32_t q_len, int32_t n_q_heads, int32_t n_kv_heads,
                                               int32_t head_dim, size_t* bytes);
