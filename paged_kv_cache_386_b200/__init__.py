@@ -635,7 +635,7 @@ def _launch(entry: str, index: int, stream, *args) -> None:
         raise PagedKVError(status, entry)
 
 
-def _on_device(index: int, *tensors) -> None:
+def _on_device(index: int, tensors) -> None:
     if index < 0:
         raise ValueError("the tensors must be CUDA tensors")
     for t in tensors:
@@ -649,26 +649,26 @@ def _flat(t: torch.Tensor, name: str) -> int:
     return t.data_ptr()
 
 
-def _heads(t: torch.Tensor, n: int, h: int, d: int, name: str) -> tuple[int, int]:
-    """Pointer and token stride (elements) of ``[num_tokens, heads, head_dim]``
-    whose heads are contiguous within a token."""
-    if t.shape != (n, h, d):
-        raise ValueError(f"{name} must be [num_tokens, heads, head_dim] = {(n, h, d)}, got {tuple(t.shape)}")
+def _token_stride(t: torch.Tensor, n: int, h: int, d: int, name: str) -> int:
+    """Elements between the tokens of ``[num_tokens, heads, head_dim]`` whose
+    heads are contiguous within a token."""
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of one token must be contiguous")
-    return t.data_ptr(), (s0 if n > 1 else h * d)
+    return s0 if n > 1 else h * d
 
 
-def _check_kv(k, v, slot_mapping) -> int:
-    if k.dtype not in _DTYPE or v.dtype != k.dtype:
+def _new_tokens(k, v, slot_mapping, n_kv: int, d: int) -> tuple[int, int]:
+    """(tokens, dtype code) of the call's keys and values."""
+    dtype, shape = _DTYPE.get(k.dtype), k.shape
+    if dtype is None or v.dtype != k.dtype:
         raise ValueError("k and v must both be float32, float16 or bfloat16")
-    if k.dim() != 3:
-        raise ValueError("k and v must be [num_tokens, n_kv_heads, head_dim]")
-    n = k.shape[0]
+    n = shape[0]
+    if shape != (n, n_kv, d) or v.shape != shape:
+        raise ValueError(f"k and v must be [num_tokens, {n_kv}, {d}], got {tuple(shape)} and {tuple(v.shape)}")
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (n,):
         raise ValueError("slot_mapping must be int64 [num_tokens]")
-    return n
+    return n, dtype
 
 
 def _empty_for(like: torch.Tensor, stream) -> torch.Tensor:
@@ -683,33 +683,36 @@ def _empty_for(like: torch.Tensor, stream) -> torch.Tensor:
 
 def _append_rope(entry: str, k, v, positions, cos_sin, slot_mapping, cache, second, n_blocks, n_kv, d, q, q_out,
                  interleaved, block_size, stream):
-    n = _check_kv(k, v, slot_mapping)
+    n, dtype = _new_tokens(k, v, slot_mapping, n_kv, d)
     if positions.dtype != torch.int64 or positions.shape != (n,):
         raise ValueError("positions must be int64 [num_tokens]")
     if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2:
         raise ValueError("cos_sin must be float32 [max_positions, rot_dim] (rotary_table)")
-    kp, ks = _heads(k, n, n_kv, d, "k")
-    vp, vs = _heads(v, n, n_kv, d, "v")
     index = cache.get_device()
-    qp, qs, op, os_, n_q = None, 0, None, 0, 0
+    qp = op = None
+    qs = os_ = n_q = 0
     if q is not None:
-        if q.dtype != k.dtype or q.dim() != 3:
+        if q.dtype != k.dtype or q.dim() != 3 or q.shape != (n, q.shape[1], d):
             raise ValueError("q must be [num_tokens, n_q_heads, head_dim] of k's dtype")
         n_q = q.shape[1]
-        qp, qs = _heads(q, n, n_q, d, "q")
+        qp, qs = q.data_ptr(), _token_stride(q, n, n_q, d, "q")
+        if q_out is None:
+            _on_device(index, (q,))
+            q_out = _empty_for(q, stream)
+            os_ = n_q * d
+        else:
+            if q_out.dtype != q.dtype or q_out.shape != q.shape:
+                raise ValueError("q_out must have q's dtype and shape")
+            os_ = _token_stride(q_out, n, n_q, d, "q_out")
+        op = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out without q")
-    _on_device(index, k, v, positions, cos_sin, slot_mapping, second, q, q_out)
-    if q is not None:
-        if q_out is None:
-            q_out = _empty_for(q, stream)
-        elif q_out.dtype != q.dtype:
-            raise ValueError("q_out must have q's dtype")
-        op, os_ = _heads(q_out, n, n_q, d, "q_out")
+    _on_device(index, (k, v, positions, cos_sin, slot_mapping, second, q, q_out))
     rows, rot = cos_sin.shape
-    _launch(entry, index, stream, qp, qs, kp, ks, vp, vs, _flat(positions, "positions"), _flat(cos_sin, "cos_sin"),
-            rows, rot, 1 if interleaved else 0, _flat(slot_mapping, "slot_mapping"), n, _flat(cache, "cache"),
-            _flat(second, "cache"), n_blocks, block_size, n_q, n_kv, d, op, os_, _DTYPE[k.dtype])
+    _launch(entry, index, stream, qp, qs, k.data_ptr(), _token_stride(k, n, n_kv, d, "k"), v.data_ptr(),
+            _token_stride(v, n, n_kv, d, "v"), _flat(positions, "positions"), _flat(cos_sin, "cos_sin"), rows, rot,
+            1 if interleaved else 0, _flat(slot_mapping, "slot_mapping"), n, _flat(cache, "cache"),
+            _flat(second, "cache"), n_blocks, block_size, n_q, n_kv, d, op, os_, dtype)
     return q_out
 
 
@@ -755,13 +758,12 @@ def paged_kv_append_fp8(k, v, slot_mapping, kv_cache, kv_scales, block_size: int
     and K or V, which grows with what is appended (its rules, and which tokens
     of a call have to be consecutive, in include/pagedkv.h)."""
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
-    n = _check_kv(k, v, slot_mapping)
-    kp, ks = _heads(k, n, n_kv, d, "k")
-    vp, vs = _heads(v, n, n_kv, d, "v")
+    n, dtype = _new_tokens(k, v, slot_mapping, n_kv, d)
     index = kv_cache.get_device()
-    _on_device(index, k, v, slot_mapping, kv_scales)
-    _launch("paged_kv_append_fp8", index, stream, kp, ks, vp, vs, _DTYPE[k.dtype], _flat(slot_mapping, "slot_mapping"),
-            n, _flat(kv_cache, "kv_cache"), _flat(kv_scales, "kv_scales"), num_blocks, block_size, n_kv, d)
+    _on_device(index, (k, v, slot_mapping, kv_scales))
+    _launch("paged_kv_append_fp8", index, stream, k.data_ptr(), _token_stride(k, n, n_kv, d, "k"), v.data_ptr(),
+            _token_stride(v, n, n_kv, d, "v"), dtype, _flat(slot_mapping, "slot_mapping"), n,
+            _flat(kv_cache, "kv_cache"), _flat(kv_scales, "kv_scales"), num_blocks, block_size, n_kv, d)
 
 
 def paged_kv_append_rope_fp8(k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales, q=None, q_out=None,
@@ -782,7 +784,7 @@ def paged_kv_copy_blocks_fp8(kv_cache, kv_scales, src_blocks, dst_blocks, block_
     if n == 0:
         return
     index = kv_cache.get_device()
-    _on_device(index, kv_scales, src_blocks, dst_blocks)
+    _on_device(index, (kv_scales, src_blocks, dst_blocks))
     _launch("paged_kv_copy_blocks_fp8", index, stream, _flat(kv_cache, "kv_cache"), _flat(kv_scales, "kv_scales"),
             _flat(src_blocks, "src_blocks"), _flat(dst_blocks, "dst_blocks"), n, num_blocks, block_size, n_kv, d)
 
@@ -820,7 +822,7 @@ def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_len
     if out is not None and (out.dtype != q.dtype or out.shape != shape or not out.is_contiguous()):
         raise ValueError("out must be a contiguous tensor of q's dtype and shape")
     index = q.get_device()
-    _on_device(index, kv_cache, kv_scales, out, block_tables, context_lens, workspace)
+    _on_device(index, (kv_cache, kv_scales, out, block_tables, context_lens, workspace))
     if out is None:
         out = _empty_for(q, stream)
     ws_ptr, ws_bytes = None, 0
