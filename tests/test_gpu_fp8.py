@@ -353,6 +353,76 @@ def test_decode_empty_batch_and_all_empty():
     assert (run_decode((q, kv, scales, tables, lens, scale)) == 0).all()
 
 
+@pytest.mark.parametrize("n_q,n_kv,d,q_len", [(1, 1, 64, 1), (9, 1, 128, 1)])
+def test_decode_of_the_largest_batch(n_q, n_kv, d, q_len):
+    lens = [1 + (7 * i) % 37 for i in range(4096)]
+    case = decode_case(lens, n_q, n_kv, d, torch.bfloat16, seed=45, q_len=q_len)
+    got = run_decode(case)
+    assert pkv.pkv_get_device_error() == 0
+    pick = list(range(0, 4096, 61)) + [4095]
+    q, kv, scales, tables, ctx, scale = case
+    values, want_scales = host(kv, scales)
+    want, bound = ref.decode(q[pick], values, want_scales, tables[pick], ctx[pick], scale)
+    assert ((got[pick].double() - want).abs() <= ref.decode_tolerance(want, bound, q.dtype)).all()
+
+
+def test_decode_refuses_a_workspace_that_does_not_fit():
+    case = decode_case([40], 8, 2, 128, torch.bfloat16, seed=46)
+    need = pkv.paged_attention_fp8_workspace_size(1, 1, 8, 2, 128)
+    for ws in (pkv.new_workspace(need - 256), pkv.new_workspace(need + 16)[16:]):
+        with pytest.raises(pkv.PagedKVError) as e:
+            run_decode(case, workspace=ws)
+        assert e.value.status == 5
+    with pytest.raises(ValueError):
+        run_decode(case, workspace=torch.zeros(need, dtype=torch.uint8))
+
+
+def test_two_graphs_share_a_workspace_in_turn():
+    cases = [decode_case([2500, 40], 8, 2, 128, torch.bfloat16, seed=47), decode_case([300] * 9, 16, 1, 64, torch.float16, seed=48)]
+    want = [run_decode(c) for c in cases]
+    ws = pkv.new_workspace(max(pkv.paged_attention_fp8_workspace_size(*a) for a in ((2, 1, 8, 2, 128), (9, 1, 16, 1, 64))))
+    graphs, outs = [], []
+    for c in cases:
+        args = [c[0].cuda(), c[1], c[2], c[3].cuda(), c[4].cuda(), c[5]]
+        out = torch.zeros_like(args[0])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            pkv.paged_attention_decode_fp8(*args, out=out, workspace=ws)
+        graphs.append((graph, args))
+        outs.append(out)
+    for i in (0, 1, 1, 0, 1, 0, 0):
+        outs[i].zero_()
+        graphs[i][0].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(outs[i].cpu()), bits(want[i]))
+    assert pkv.pkv_get_device_error() == 0
+
+
+def test_append_into_a_graph():
+    """A captured append, replayed on new tokens and slots, against the eager one."""
+    g = torch.Generator().manual_seed(49)
+    table = pkv.rotary_table(64, 128, device="cuda")
+    k, v, q = (torch.randn((6, h, 128), generator=g).bfloat16().cuda() for h in (2, 2, 8))
+    pos, slots = torch.arange(6).cuda(), (torch.arange(6) + 16).cuda()
+    kv, scales = random_cache(4, 2, 128, 50)
+    q_out = torch.zeros_like(q)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        pkv.paged_kv_append_rope_fp8(k, v, pos, table, slots, kv, scales, q=q, q_out=q_out)
+    for step in range(3):
+        for t in (k, v, q):
+            t.copy_(torch.randn(t.shape, generator=g).bfloat16() * (step + 1))
+        slots.copy_(torch.tensor([0, 1, 2, -1, 40, 41]) + 3 * step)
+        if step:
+            slots[3] = -1
+        kv2, scales2 = kv.clone(), scales.clone()
+        want_q = pkv.paged_kv_append_rope_fp8(k, v, pos, table, slots, kv2, scales2, q=q)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(bits(q_out), bits(want_q)) and torch.equal(scales, scales2)
+        assert torch.equal(kv.view(torch.uint8), kv2.view(torch.uint8))
+
+
 def test_large_pool_offsets_pass_32_bits():
     """A pool of more than 4 GiB of codes: blocks at its far end."""
     n_kv, d, blocks = 32, 128, 36000  # 4.7 GB
