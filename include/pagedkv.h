@@ -612,6 +612,7 @@ pkv_status paged_kv_copy_blocks_fp8(uint8_t* kv_cache, float* kv_scales, const i
  * their block's scales.
  *
  *   q, out    : device, [batch][q_len][n_q_heads][head_dim], f16 or bf16
+ *   num_blocks: with num_blocks * n_kv_heads < 2^31
  *   q_len     : 1 .. 16, the last tokens of every context; query i sees tokens
  *               j < context_lens[b] - q_len + i + 1
  *   kv_scales : of the blocks read: positive and normal, as the appends write

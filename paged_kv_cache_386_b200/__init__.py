@@ -830,6 +830,6 @@ def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_len
         ws_ptr, ws_bytes = _flat(workspace, "workspace"), workspace.numel() * workspace.element_size()
     _launch("paged_attention_decode_fp8", index, stream, _flat(q, "q"), _flat(kv_cache, "kv_cache"),
             _flat(kv_scales, "kv_scales"), _flat(block_tables, "block_tables"), block_tables.shape[1],
-            _flat(context_lens, "context_lens"), B, q_len, num_blocks, scale, n_q, n_kv, d, block_size, out.data_ptr(),
+            _flat(context_lens, "context_lens"), B, q_len, num_blocks, float(scale), n_q, n_kv, d, block_size, out.data_ptr(),
             _DTYPE[q.dtype], ws_ptr, ws_bytes)
     return out

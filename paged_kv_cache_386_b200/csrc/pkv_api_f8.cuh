@@ -53,8 +53,9 @@ pkv_status rope_append_params(const void* q, int64_t q_stride, const void* k, in
 }
 
 // Heads that one thread of the rotation walks, sharing a token's cosines
-// and sines: as many as leave about two threads for every one the device
-// holds, at most 8.
+// and sines: as many as leave a thread for every one the device holds, at
+// most 8.  (8192 tokens, 32/8 heads: 36.4 us, 48.4 with one head a thread; one
+// token: 2.3 us, 4.6 with eight.)
 int rope_heads_per_thread(int64_t columns, int heads, int sm_count) {
   const int64_t want = static_cast<int64_t>(sm_count) * 2048;
   for (int hp = 8; hp > 1; hp /= 2)
@@ -88,7 +89,8 @@ pkv_status append_f8(const RopeAppendParams& rp, pkv_dtype dtype, uint8_t* kv_ca
   p.scales = kv_scales;
   // A token a pair of warps while all of them fit the device at once (a decode
   // step: every token its own run); else 16, so that a prompt's warps are not
-  // mostly ones without a run start.
+  // mostly ones without a run start.  (64 single tokens, 32/8 heads: 4.3 us,
+  // 36.7 with 16; 16384 prompt tokens, 8 heads: 20.8 us, 117 with one.)
   p.tokens_per_pair = static_cast<int64_t>(rp.num_tokens) * rp.n_kv <= static_cast<int64_t>(di.sm_count) * 16 ? 1 : 16;
   p.token_chunks = (rp.num_tokens + p.tokens_per_pair - 1) / p.tokens_per_pair;
   const int64_t items = static_cast<int64_t>(p.token_chunks) * rp.n_kv * (p.tokens_per_pair == 1 ? 2 : 1);
@@ -110,7 +112,9 @@ pkv_status append_f8(const RopeAppendParams& rp, pkv_dtype dtype, uint8_t* kv_ca
   }
 }
 
-// Rows of a segment: all rows of a kv head up to 16, else equal parts.
+// Rows of a segment: all rows of a kv head up to 16, else equal parts.  (16 rows,
+// 32 x 4 queries: 42.7 us, 52.1 as twice 8; 12 rows, 64 mixed lengths: 67.1,
+// 90.6 as twice 6.  4 rows in the kernel of 16: 65.3, 54.5 in that of 8.)
 void decode_f8_segments(int total_rows, int* nseg, int* rows) {
   *nseg = (total_rows + 15) / 16;
   *rows = (total_rows + *nseg - 1) / *nseg;

@@ -38,12 +38,18 @@
 namespace pkv {
 
 constexpr int kF8MaxStages = 6;                       // ring slots of a warp
-constexpr int kF8MinSlots = 2;                        // slots that make a unit worth its merge
+// Slots that make a unit worth its merge (one sequence of 4096 tokens, 32/8 heads:
+// 14.7 us with 1, 13.6 with 2, 16.7 with 4).
+constexpr int kF8MinSlots = 2;
 // A segment's fixed work, in tiles.  Measured with none: the slowest warp of 256
 // mixed lengths of 1 to 1300 tokens, 32/32 heads, ended 25% after the mean (263 us,
 // 216 with two); with 16 rows, seven against two: 46.4 -> 42.8 us (32 x 4 queries).
 __host__ __device__ constexpr int f8_seg_slots(int NR) { return NR == 1 ? 2 : 7; }
-constexpr int kF8W1 = 16, kF8W2 = 8;                  // warps of a CTA with up to 8 rows, with 16
+// Warps of a CTA with up to 8 rows a segment, and with up to 16: as many as their
+// registers allow (128 and 255 a thread).  8 rows, 64 mixed lengths: 58.0 us with
+// 12 warps, 57.6 with 16; 4 x 131072: 186, 178.  16 rows, 32 x 4 queries: 42.1 with
+// 8, 44.9 with 12.
+constexpr int kF8W1 = 16, kF8W2 = 8;
 constexpr int kF8HeaderBytes = 4096;                  // workspace: a counter per CTA
 constexpr float kF8RefBelow = 7.f, kF8RefSlack = 14.f;
 
@@ -904,10 +910,9 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
 
   // ---------------- the CTA's shared segments ----------------
   const int A = bnd[0], E = bnd[n_units], ng = n_groups;
-  // A warp a row while the warps suffice (long contexts: one or two groups of
-  // many pieces), else four rows a warp (many groups of two pieces).
-  const bool split = ng * p.rows <= W;
-  const int items = split ? p.rows : (p.rows + 3) / 4;
+  // Four rows a warp.  (A row a warp, its pieces shared by the groups of lanes:
+  // 59 us against 43 for 32 x 4 queries, no gain where there are few rows.)
+  const int items = (p.rows + 3) / 4;
   for (int i = warp; i < ng * items; i += W) {
     const F8Group& gr = groups[i / items];
     F8Pieces pc;  // in the rings; the last one in its unit's record if more follows it there
@@ -921,10 +926,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     }
     float* to = nullptr;
     if (gr.st < A || gr.en > E) to = p.cta_recs + (static_cast<size_t>(blockIdx.x) * 2 + (gr.st < A ? 0 : 1)) * p.rec_floats;
-    if (split)
-      f8_merge<D, kBf16, true>(p, pc, i % items, gr.rows, to, gr.b, gr.kvh, gr.first);
-    else
-      f8_merge<D, kBf16, false>(p, pc, i % items * 4, gr.rows, to, gr.b, gr.kvh, gr.first);
+    f8_merge<D, kBf16, false>(p, pc, i % items * 4, gr.rows, to, gr.b, gr.kvh, gr.first);
   }
 
   // ---------------- segments shared with other CTAs ----------------
@@ -958,6 +960,8 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     pc.base = p.cta_recs + static_cast<size_t>(gr.c0) * pc.stride;
     pc.first = pc.base + p.rec_floats;
     pc.last = nullptr;
+    // Many shares: a warp a row (one sequence of 4096: 13.6 us, 18.7 with four
+    // rows a warp); few: four rows a warp (32 x 4 queries: 42.7 us, 45.0).
     if (pc.n > 4) {
       for (int i = warp; i < gr.rows; i += W) f8_merge<D, kBf16, true>(p, pc, i, gr.rows, nullptr, gr.b, gr.kvh, gr.first);
     } else {
