@@ -132,17 +132,18 @@ pkv_status launch_decode_f8(const CUtensorMap& map, DecodeF8Params p, const Devi
   int dev = 0;
   cudaFuncAttributes fa;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return PKV_ERR_CUDA;
-  constexpr int kStatic = 1024;  // more than the kernel's static shared memory
+  constexpr int kStatic = 2048;  // more than the kernel's static shared memory
   if (!opted_in[dev]) {
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.sharedSizeBytes > kStatic ||
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin - kStatic) != cudaSuccess)
       return PKV_ERR_CUDA;
     opted_in[dev] = true;
   }
-  p.stages = kF8MaxStages;
+  p.stages = f8_stages(D, NR);  // fewer where a large batch's lengths take their place
+  const size_t limit = di.smem_optin - kStatic;
   auto smem = [&] { return f8_smem_bytes(D, f8_warps(NR), p.stages, p.rows, p.batch); };
-  while (smem() > static_cast<size_t>(di.smem_optin - kStatic)) --p.stages;
-  if (p.stages * f8_tile_bytes(D) < p.rec_floats * 4) return PKV_ERR_UNSUPPORTED;  // a warp's ring holds a record
+  while (p.stages > 1 && smem() > limit) --p.stages;
+  if (smem() > limit || p.stages * f8_tile_bytes(D) < p.rec_floats * 4) return PKV_ERR_UNSUPPORTED;  // a ring holds a record
   kern<<<di.sm_count, f8_warps(NR) * 32, smem(), s>>>(map, p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }

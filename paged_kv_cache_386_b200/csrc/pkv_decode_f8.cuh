@@ -37,7 +37,10 @@
 
 namespace pkv {
 
-constexpr int kF8MaxStages = 6;                       // ring slots of a warp
+// Tiles under way on an SM.  More only lengthens the memory's queues: 256 mixed
+// lengths, 32/32 heads of 128: 223 us with 192 KiB, 214 with 128; 4 x 131072: 175,
+// 168.5; heads of 64: 36.5, 36.1 (37.9 with 64); 16 rows: 42.0, 41.5 (44.9 with 64).
+constexpr int kF8RingBytes = 128 * 1024;
 // Slots that make a unit worth its merge (one sequence of 4096 tokens, 32/8 heads:
 // 14.7 us with 1, 13.6 with 2, 16.7 with 4).
 constexpr int kF8MinSlots = 2;
@@ -596,12 +599,14 @@ __device__ __forceinline__ void f8_next_segment(F8Walk& w, const int* prefix, co
   }
 }
 
-// Where unit u's slots begin.
+// Where unit u's slots begin, and (but for the end of all) the tile there.
 template <int kSeg>
-__device__ __forceinline__ int f8_unit_begin(const Sched& sc, int u, const int* prefix, const int* ctxs, int B) {
+__device__ __forceinline__ int f8_unit_begin(const Sched& sc, int u, const int* prefix, const int* ctxs, int B,
+                                             F8Walk* at) {
   const int k = unit_begin(sc, u);
-  if (u == 0 || u >= sc.U) return k;
+  if (u >= sc.U) return k;
   const F8Walk w = f8_find<kSeg>(prefix, ctxs, B, k);
+  *at = w;
   return w.j == 0 ? w.st : k;
 }
 
@@ -651,6 +656,9 @@ __device__ __noinline__ void f8_find_groups(const DecodeF8Params& p, const Sched
 // Warps of a CTA, each a unit.
 __host__ __device__ constexpr int f8_warps(int NR) { return NR == 1 ? kF8W1 : kF8W2; }
 
+// Ring slots of a warp (2 to 8).
+__host__ __device__ constexpr int f8_stages(int D, int NR) { return kF8RingBytes / (f8_warps(NR) * f8_tile_bytes(D)); }
+
 // Shared memory: each warp's ring, its Q rows; a barrier, a scale pair and a flag of each ring slot; lengths.
 __host__ __device__ constexpr size_t f8_smem_bytes(int D, int W, int stages, int rows, int batch) {
   return 1024 + static_cast<size_t>(W) * (stages * (f8_tile_bytes(D) + 20) + rows * D * 2) + 16 +
@@ -676,7 +684,8 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   int* prefix = const_cast<int*>(abort_flag) + 4;  // [batch + 1]: slots before each sequence
   int* ctxs = prefix + p.batch + 1;                // [batch]
   __shared__ int warp_sums[W];
-  __shared__ int bnd[W + 1];  // where this CTA's units begin
+  __shared__ int bnd[W + 1];  // where this CTA's units begin, and the tiles there
+  __shared__ F8Walk starts[W + 1];
   __shared__ F8Group groups[W + 1];
   __shared__ int n_groups;
   __shared__ int last_of[2];  // this CTA finishes: the segment from before it, the one that goes on behind it
@@ -740,7 +749,8 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   const int per_cta = (sc.U + gridDim.x - 1) / static_cast<int>(gridDim.x);
   const int u0 = blockIdx.x * per_cta, n_units = min(sc.U - u0, per_cta);  // this CTA's units
   if (T == 0 || n_units <= 0) return;
-  if (threadIdx.x <= n_units) bnd[lane] = f8_unit_begin<kSeg>(sc, u0 + lane, prefix, ctxs, B);
+  if (threadIdx.x <= n_units)
+    bnd[threadIdx.x] = f8_unit_begin<kSeg>(sc, u0 + threadIdx.x, prefix, ctxs, B, &starts[threadIdx.x]);
   __syncthreads();
 
   // Rows of segment hg of a sequence: kv head, first of its rows, how many.
@@ -764,7 +774,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
         cp_async_16(qbuf + i * 16, p.q + f8_row_at(p, b, kvh, first + i / kChunks, D) + (i % kChunks) * 8);
       cp_async_commit();
     };
-    F8Walk wk = f8_find<kSeg>(prefix, ctxs, B, k0);
+    F8Walk wk = starts[warp];
     fetch_q(wk.b, wk.hg);  // in front of the copies that fill the memory's queues
 
     // Issue side: the warp copies its own tiles, a ring ahead of their use.
