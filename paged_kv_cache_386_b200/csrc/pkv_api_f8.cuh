@@ -139,12 +139,9 @@ pkv_status launch_decode_f8(const CUtensorMap& map, DecodeF8Params p, const Devi
       return PKV_ERR_CUDA;
     opted_in[dev] = true;
   }
-  p.stages = f8_stages(D, NR);  // fewer where a large batch's lengths take their place
-  const size_t limit = di.smem_optin - kStatic;
-  auto smem = [&] { return f8_smem_bytes(D, f8_warps(NR), p.stages, p.rows, p.batch); };
-  while (p.stages > 1 && smem() > limit) --p.stages;
-  if (smem() > limit || p.stages * f8_tile_bytes(D) < p.rec_floats * 4) return PKV_ERR_UNSUPPORTED;  // a ring holds a record
-  kern<<<di.sm_count, f8_warps(NR) * 32, smem(), s>>>(map, p);
+  const size_t smem = f8_smem_bytes(D, NR, p.rows, p.batch);
+  if (smem > static_cast<size_t>(di.smem_optin - kStatic)) return PKV_ERR_UNSUPPORTED;
+  kern<<<di.sm_count, f8_warps(NR) * 32, smem, s>>>(map, p);
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

@@ -71,7 +71,6 @@ struct DecodeF8Params {
   int32_t rows;        // rows of a segment (the last one of a kv head may have fewer)
   int32_t nseg;        // segments of a kv head
   int32_t ng;          // segments of a sequence, n_kv * nseg
-  int32_t stages;
   int32_t rec_floats;  // rows * (D + 4)
   float scale_log2;
   uint64_t wait_limit_ns;
@@ -659,9 +658,9 @@ __host__ __device__ constexpr int f8_warps(int NR) { return NR == 1 ? kF8W1 : kF
 // Ring slots of a warp (2 to 8).
 __host__ __device__ constexpr int f8_stages(int D, int NR) { return kF8RingBytes / (f8_warps(NR) * f8_tile_bytes(D)); }
 
-// Shared memory: each warp's ring, its Q rows; a barrier, a scale pair and a flag of each ring slot; lengths.
-__host__ __device__ constexpr size_t f8_smem_bytes(int D, int W, int stages, int rows, int batch) {
-  return 1024 + static_cast<size_t>(W) * (stages * (f8_tile_bytes(D) + 20) + rows * D * 2) + 16 +
+// Shared memory: each warp's ring, its Q rows, a barrier, a scale pair and a flag of each ring slot; lengths.
+__host__ __device__ constexpr size_t f8_smem_bytes(int D, int NR, int rows, int batch) {
+  return 1024 + kF8RingBytes + static_cast<size_t>(f8_warps(NR)) * (f8_stages(D, NR) * 20 + rows * D * 2) + 16 +
          (2 * static_cast<size_t>(batch) + 1) * 4;
 }
 
@@ -671,11 +670,15 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   constexpr int kTile = f8_tile_bytes(D);
   constexpr int W = f8_warps(NR), kThreads = W * 32, kSeg = f8_seg_slots(NR);
   using Consumer = F8Consumer<D, NR, kBf16>;
+  constexpr int RS = Consumer::RS;
 
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw = smem_u32(smem_raw);
   uint8_t* rings = smem_raw + (((raw + 1023u) & ~1023u) - raw);
-  const int S = p.stages, q_bytes = p.rows * D * 2, n_slots = W * S;
+  constexpr int S = f8_stages(D, NR), n_slots = W * S;
+  static_assert(S >= 2 && S * kTile >= 8 * NR * RS * 4, "a step's tiles, and a record, in a warp's ring");
+  static_assert(n_slots <= kThreads, "a thread for each barrier's set-up");
+  const int q_bytes = p.rows * D * 2;
   uint8_t* qbufs = rings + static_cast<size_t>(n_slots) * kTile;
   uint64_t* full_bar = reinterpret_cast<uint64_t*>(qbufs + W * q_bytes);  // [W][S]: the slot's copies have landed
   float2* slot_scale = reinterpret_cast<float2*>(full_bar + n_slots);
