@@ -20,6 +20,7 @@ from __future__ import annotations
 
 import ctypes
 from pathlib import Path
+from types import SimpleNamespace
 
 import torch
 
@@ -614,9 +615,30 @@ def rotary_table(max_positions: int, rot_dim: int, theta: float = 10000.0, devic
     return torch.cat((angle.cos(), angle.sin()), 1).float()
 
 
-# The calls below are host-bound at a decode step's sizes, so their checks read
-# each tensor's shape and strides once, and the device is only switched when
-# another one is current.
+# The calls below are host-bound at a decode step's sizes: what is plain (CUDA
+# tensors on the current device and stream, with the right types, shapes and
+# strides) goes through the extension `_binding`, which returns NotImplemented
+# for all else; the Python functions then check, report and handle the call, and
+# do so for every call where the extension is not built.
+_ext = None
+
+
+def _quick():
+    """The extension, bound to the library; False if it is not built."""
+    global _ext
+    if _ext is None:
+        lib = _load()
+        try:
+            from ._binding import append_fp8, append_rope, bind, decode_fp8
+        except ImportError:
+            _ext = False
+            return False
+        bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "paged_kv_append_rope", "paged_kv_append_rope_fp8", "paged_kv_append_fp8", "paged_attention_decode_fp8")))
+        _ext = SimpleNamespace(append_rope=append_rope, append_fp8=append_fp8, decode_fp8=decode_fp8)
+    return _ext
+
+
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
@@ -726,6 +748,10 @@ def paged_kv_append_rope(k, v, positions, cos_sin, slot_mapping, k_cache, v_cach
     projection (heads of a token contiguous).  Returns the rotated queries in
     ``q_out`` (a new tensor by default; ``q_out=q`` rotates in place), or None
     without ``q``."""
+    if stream is None and block_size == 16 and (quick := _ext or _quick()):
+        done = quick.append_rope(k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q, q_out, interleaved, False)
+        if done is not NotImplemented:
+            return done
     num_blocks, n_kv, bs, d = k_cache.shape
     if bs != block_size or v_cache.shape != k_cache.shape:
         raise ValueError("cache shapes disagree")
@@ -757,6 +783,9 @@ def paged_kv_append_fp8(k, v, slot_mapping, kv_cache, kv_scales, block_size: int
     (in place): e4m3 codes with one power-of-two scale for each block, kv head
     and K or V, which grows with what is appended (its rules, and which tokens
     of a call have to be consecutive, in include/pagedkv.h)."""
+    if stream is None and block_size == 16 and (quick := _ext or _quick()):
+        if quick.append_fp8(k, v, slot_mapping, kv_cache, kv_scales) is not NotImplemented:
+            return
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
     n, dtype = _new_tokens(k, v, slot_mapping, n_kv, d)
     index = kv_cache.get_device()
@@ -770,6 +799,10 @@ def paged_kv_append_rope_fp8(k, v, positions, cos_sin, slot_mapping, kv_cache, k
                              interleaved: bool = False, block_size: int = 16, stream=None):
     """paged_kv_append_rope into the FP8 cache (keys are quantised from their
     fp32 rotation); returns the rotated queries as there."""
+    if stream is None and block_size == 16 and (quick := _ext or _quick()):
+        done = quick.append_rope(k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales, q, q_out, interleaved, True)
+        if done is not NotImplemented:
+            return done
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
     return _append_rope("paged_kv_append_rope_fp8", k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales,
                         num_blocks, n_kv, d, q, q_out, interleaved, block_size, stream)
@@ -805,6 +838,10 @@ def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_len
     its context up to position ``ctx - q_len + i``), float16 or bfloat16.
     ``workspace``: :func:`new_workspace` of paged_attention_fp8_workspace_size
     bytes, for one call at a time.  Returns ``out`` (shape and dtype of q)."""
+    if stream is None and block_size == 16 and (quick := _ext or _quick()):
+        done = quick.decode_fp8(q, kv_cache, kv_scales, block_tables, context_lens, scale, out, workspace)
+        if done is not NotImplemented:
+            return done
     num_blocks, n_kv, d = _fp8_shape(kv_cache, kv_scales, block_size)
     shape = q.shape
     if len(shape) == 3:

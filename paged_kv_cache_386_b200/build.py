@@ -1,7 +1,8 @@
-"""Build libpagedkv.so (the CUDA library behind include/pagedkv.h) for sm_100a.
+"""Build libpagedkv.so (the CUDA library behind include/pagedkv.h) for sm_100a,
+and ``_binding.so`` (the quick way from torch tensors to its host-bound calls).
 
-``python -m paged_kv_cache_386_b200.build`` compiles in place with nvcc; the
-library links the CUDA runtime statically, so it loads without a GPU.
+``python -m paged_kv_cache_386_b200.build`` compiles in place with nvcc and g++;
+the library links the CUDA runtime statically, so it loads without a GPU.
 """
 
 from __future__ import annotations
@@ -10,6 +11,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -18,6 +20,8 @@ CSRC = PKG / "csrc"
 LIB = PKG / "libpagedkv.so"
 SOURCES = [CSRC / "pkv_api.cu", CSRC / "pkv_block_manager.cpp"]
 HEADERS = sorted(CSRC.glob("*.cuh")) + [ROOT / "include" / "pagedkv.h"]
+BINDING = PKG / "_binding.so"
+BINDING_SOURCES = [CSRC / "pkv_binding.cpp", ROOT / "include" / "pagedkv.h"]
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
@@ -38,16 +42,29 @@ def command(out: Path = LIB, verbose_ptxas: bool = False) -> list[str]:
     return cmd + ["-o", str(out), *map(str, SOURCES)]
 
 
-def stale(out: Path = LIB) -> bool:
+def binding_command(out: Path = BINDING) -> list[str]:
+    import torch
+
+    torch_dir = Path(torch.__file__).resolve().parent
+    cuda = Path(nvcc()).resolve().parent.parent
+    return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            "-I", str(ROOT / "include"), "-I", sysconfig.get_paths()["include"], "-I", str(torch_dir / "include"),
+            "-I", str(cuda / "include"), "-o", str(out), str(BINDING_SOURCES[0]), "-L", str(torch_dir / "lib"),
+            f"-Wl,-rpath,{torch_dir / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
+
+
+def stale(out: Path = LIB, sources=None) -> bool:
     if not out.exists():
         return True
     t = out.stat().st_mtime
-    return any(p.stat().st_mtime > t for p in SOURCES + HEADERS)
+    return any(p.stat().st_mtime > t for p in (SOURCES + HEADERS if sources is None else sources))
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
     if force or stale():
         subprocess.run(command(verbose_ptxas=verbose_ptxas), check=True)
+    if force or stale(BINDING, BINDING_SOURCES):
+        subprocess.run(binding_command(), check=True)
     return LIB
 
 
