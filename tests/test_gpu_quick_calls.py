@@ -158,3 +158,37 @@ def test_current_stream_and_graph(ext):
     want_q = e.rope_fp8(q=q)
     assert torch.equal(bits(q2), bits(want_q)) and torch.equal(bits(out), bits(e.decode(want_q[-1:])))
     assert torch.equal(c.kv.view(torch.uint8), e.kv.view(torch.uint8)) and torch.equal(c.sc, e.sc)
+
+
+@pytest.mark.gpu
+def test_threads_with_a_stream_each(ext):
+    """Calls release the interpreter while they launch: threads do not disturb one another."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    want = {seed: Case(seed=seed).everything() for seed in range(4)}
+    cases = {seed: [Case(seed=seed) for _ in range(8)] for seed in want}
+    torch.cuda.synchronize()
+
+    def work(seed):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got = [c.everything() for c in cases[seed]]
+            torch.cuda.current_stream().synchronize()
+        return got
+
+    with ThreadPoolExecutor(4) as pool:
+        for seed, results in zip(want, pool.map(work, want), strict=True):
+            for got in results:
+                assert all(torch.equal(x, y) for x, y in zip(got, want[seed], strict=True))
+
+
+@pytest.mark.gpu
+def test_one_row_for_all_tokens(ext, checked):
+    """Inputs whose tokens are one broadcast row; an output may not be one."""
+    a, b = Case(), Case()
+    for c in (a, b):
+        c.k, c.v, c.q = (x[:1].expand(len(c.slots), -1, -1) for x in (c.k, c.v, c.q))
+    got, want = a.rope_fp8(q=a.q), checked(lambda: b.rope_fp8(q=b.q))
+    assert torch.equal(bits(got), bits(want)) and torch.equal(a.sc, b.sc)
+    assert torch.equal(a.kv.view(torch.uint8), b.kv.view(torch.uint8))
+    with pytest.raises(pkv.PagedKVError):
+        a.rope_fp8(q=a.q, q_out=a.q)
