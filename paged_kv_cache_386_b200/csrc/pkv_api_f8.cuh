@@ -63,16 +63,34 @@ int rope_heads_per_thread(int64_t columns, int heads, int sm_count) {
   return 1;
 }
 
+// The launch overlaps the end of the kernel in front on the stream, whose writes
+// the kernel waits for itself.  Calls back to back on a stream, one token's
+// rotating append: 2.0 us, 4.1 without; a step's FP8 append 3.7, 6.2; one sequence's
+// decode 12.6, 14.4; in a graph 0.2 to 0.6 us less.  (The next launch allowed from
+// a kernel's start on, not from its end: 2.2, 4.3 and 12.9, its blocks are in the way.)
+template <typename... P>
+pkv_status launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem, cudaStream_t s, const P&... p) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  cudaLaunchAttribute a[1];
+  a[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kern, p...) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 template <int DT>
 pkv_status launch_append_f8(const AppendF8Params& p, unsigned grid, cudaStream_t s) {
   const bool rope = p.rp.rope.rot > 0;
   if (p.rp.head_dim == 64)
-    rope ? pkv_append_f8_kernel<DT, 64, true><<<grid, 256, 0, s>>>(p)
-         : pkv_append_f8_kernel<DT, 64, false><<<grid, 256, 0, s>>>(p);
-  else
-    rope ? pkv_append_f8_kernel<DT, 128, true><<<grid, 256, 0, s>>>(p)
-         : pkv_append_f8_kernel<DT, 128, false><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+    return launch_early(rope ? pkv_append_f8_kernel<DT, 64, true> : pkv_append_f8_kernel<DT, 64, false>, grid, 256, 0,
+                        s, p);
+  return launch_early(rope ? pkv_append_f8_kernel<DT, 128, true> : pkv_append_f8_kernel<DT, 128, false>, grid, 256, 0,
+                      s, p);
 }
 
 // paged_kv_append_fp8 and paged_kv_append_rope_fp8 (rot_dim 0: no rotation, no queries).
@@ -141,8 +159,7 @@ pkv_status launch_decode_f8(const CUtensorMap& map, DecodeF8Params p, const Devi
   }
   const size_t smem = f8_smem_bytes(D, NR, p.rows, p.batch);
   if (smem > static_cast<size_t>(di.smem_optin - kStatic)) return PKV_ERR_UNSUPPORTED;
-  kern<<<di.sm_count, f8_warps(NR) * 32, smem, s>>>(map, p);
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return launch_early(kern, di.sm_count, f8_warps(NR) * 32, smem, s, map, p);
 }
 
 template <bool kBf16>
@@ -184,11 +201,10 @@ pkv_status paged_kv_append_rope(const void* q, int64_t q_stride, const void* k, 
   const dim3 grid(static_cast<unsigned>((columns + 255) / 256), static_cast<unsigned>(groups));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   switch (dtype) {
-    case PKV_F32: pkv_append_rope_kernel<kF32><<<grid, 256, 0, s>>>(p); break;
-    case PKV_F16: pkv_append_rope_kernel<kF16><<<grid, 256, 0, s>>>(p); break;
-    default: pkv_append_rope_kernel<kBF16><<<grid, 256, 0, s>>>(p); break;
+    case PKV_F32: return launch_early(pkv_append_rope_kernel<kF32>, grid, 256, 0, s, p);
+    case PKV_F16: return launch_early(pkv_append_rope_kernel<kF16>, grid, 256, 0, s, p);
+    default: return launch_early(pkv_append_rope_kernel<kBF16>, grid, 256, 0, s, p);
   }
-  return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status paged_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, pkv_dtype dtype,

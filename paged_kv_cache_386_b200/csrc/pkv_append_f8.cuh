@@ -17,6 +17,11 @@
 
 namespace pkv {
 
+// These kernels are launched while the kernel in front of them on the stream ends
+// (launch_early), and wait here until its writes can be seen, before they read or
+// write any memory but their own shared memory.
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Sixteen elements of a head row as fp32: two pieces of eight consecutive dims.
 template <int DT>
 struct Piece8 {
@@ -235,6 +240,7 @@ __device__ __forceinline__ void rope_append_item(const RopeAppendParams& p, uint
 
 template <int DT>
 __global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_rope_kernel(const RopeAppendParams p) {
+  wait_for_kernel_before();
   rope_append_item<DT>(p, blockIdx.x * 256u + threadIdx.x, blockIdx.y, p.n_q + 2 * p.n_kv);
 }
 
@@ -459,7 +465,7 @@ __device__ __forceinline__ void append_f8_rows(const AppendF8Params& p, int64_t 
 // D / 16 lanes hold a row, all rows of the half at once, 16 registers of 16-bit
 // data: what bounds a prompt is how many rows are under way, and 64 registers
 // a thread let four CTAs fit an SM.  (One warp a run, all of it as fp32: 128
-// registers, 32.2 us for 16384 bf16 tokens of 8 heads of 128; now 20.8, the
+// registers, 32.2 us for 16384 bf16 tokens of 8 heads of 128; now 20.4, the
 // floor is 15.4.  The next head's rows requested ahead, or the call's rows
 // before its slots are known: more registers, slower.)
 template <int DT, int D, bool kRope>
@@ -516,6 +522,7 @@ __device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t b
 
 template <int DT, int D, bool kRope>
 __global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_f8_kernel(const AppendF8Params p) {
+  wait_for_kernel_before();
   const RopeAppendParams& rp = p.rp;
   if (kRope && static_cast<int>(blockIdx.x) >= p.kv_ctas) {  // queries
     const uint32_t i = blockIdx.x - p.kv_ctas;

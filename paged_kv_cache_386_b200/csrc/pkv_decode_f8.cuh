@@ -704,6 +704,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     *abort_flag = 0;
     tma_prefetch_desc(&tm);
   }
+  wait_for_kernel_before();
 
   {
     const int per = (B + kThreads - 1) / kThreads;
