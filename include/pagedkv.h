@@ -84,8 +84,9 @@ typedef enum pkv_status {
 #define PKV_DEVERR_SLOT 0x4u       /* slot >= num_blocks * block_size: the token was not written */
 #define PKV_DEVERR_TIMEOUT 0x8u    /* a bounded in-kernel wait (2 s by default) gave up: that launch's
                                       output is undefined (the kernel drained its own copies and ended) */
-#define PKV_DEVERR_SCHEDULE 0x10u  /* the decode workspace was not zero-filled before its first use: that
-                                      launch's result is wrong (the workspace is zeroed again) */
+#define PKV_DEVERR_SCHEDULE 0x10u  /* the workspace of a decode with balancing chunks was not zero-filled
+                                      before its first use: that launch's result is wrong (the workspace is
+                                      zeroed again) */
 #define PKV_DEVERR_POSITION 0x20u  /* position outside the rotation table: the token was left out (no row of
                                       it was written) */
 
@@ -618,9 +619,9 @@ pkv_status paged_kv_copy_blocks_fp8(uint8_t* kv_cache, float* kv_scales, const i
  *   kv_scales : of the blocks read: positive and normal, as the appends write
  *               them (any such value, not only powers of two)
  *   workspace : paged_attention_fp8_workspace_size() bytes on the current
- *               device, 256-byte aligned, zero-filled before its first use and
- *               for one call at a time (each call leaves it ready for the
- *               next, of any sizes that fit it); NULL allocates it on `stream`.
+ *               device, 256-byte aligned, for one call at a time.  It may hold
+ *               anything (no clearing, no state from call to call) and serves
+ *               calls of any sizes that fit it; NULL allocates it on `stream`.
  * A block id or a context length out of range is treated as in
  * paged_attention_decode_mq.  A NaN in a key or value reaches the rows that see
  * its token, and no others.

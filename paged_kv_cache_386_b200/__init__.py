@@ -836,8 +836,8 @@ def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_len
     """paged_attention_decode over the FP8 cache.  ``q`` is ``[batch, n_q, d]``,
     or ``[batch, q_len, n_q, d]`` for several queries per sequence (query i sees
     its context up to position ``ctx - q_len + i``), float16 or bfloat16.
-    ``workspace``: :func:`new_workspace` of paged_attention_fp8_workspace_size
-    bytes, for one call at a time.  Returns ``out`` (shape and dtype of q)."""
+    ``workspace``: paged_attention_fp8_workspace_size bytes (of any contents),
+    for one call at a time.  Returns ``out`` (shape and dtype of q)."""
     if stream is None and block_size == 16 and (quick := _ext or _quick()):
         done = quick.decode_fp8(q, kv_cache, kv_scales, block_tables, context_lens, scale, out, workspace)
         if done is not NotImplemented:

@@ -138,6 +138,17 @@ void decode_f8_segments(int total_rows, int* nseg, int* rows) {
   *rows = (total_rows + *nseg - 1) / *nseg;
 }
 
+// A call's step of the arrivals in its workspace: 1 in the bits from 48 on, below them
+// a pseudo-random odd number of 39 bits (its multiples for up to 512 arrivals stay
+// below bit 48).  What a workspace held before is taken for arrivals of the call,
+// whose word would have to be 0 or a multiple, with a chance of 2^-38 a word.
+unsigned long long f8_arrival() {
+  static std::atomic<uint64_t> calls{static_cast<uint64_t>(std::chrono::steady_clock::now().time_since_epoch().count())};
+  uint64_t x = (calls.fetch_add(1, std::memory_order_relaxed) * 2 + 1) * 0x9e3779b97f4a7c15ull;
+  x ^= x >> 32;
+  return (1ull << 48) | (x & ((1ull << 39) - 1)) | 1ull;
+}
+
 size_t decode_f8_workspace(int sm_count, int rows, int head_dim) {
   const size_t records = static_cast<size_t>(sm_count) * (f8_warps(rows <= 8 ? 1 : 2) + 2);  // a unit's each, two of each CTA
   return kF8HeaderBytes + records * rows * (head_dim + 4) * sizeof(float);
@@ -289,7 +300,7 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
   if (static_cast<int64_t>(num_blocks) * n_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;  // a TMA coordinate
   DeviceInfo di;
   if (device_info(&di) != PKV_OK) return PKV_ERR_CUDA;
-  if (static_cast<size_t>(di.sm_count) * sizeof(unsigned int) > kF8HeaderBytes) return PKV_ERR_UNSUPPORTED;
+  if (static_cast<size_t>(di.sm_count) * sizeof(unsigned long long) > kF8HeaderBytes) return PKV_ERR_UNSUPPORTED;
   DecodeF8Params p = {};
   p.q = static_cast<const uint16_t*>(q);
   p.out = static_cast<uint16_t*>(out);
@@ -323,12 +334,9 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
     void* at = nullptr;
     if (cudaMallocAsync(&at, need, s) != cudaSuccess) return PKV_ERR_CUDA;
     ws = static_cast<uint8_t*>(at);
-    if (cudaMemsetAsync(ws, 0, kF8HeaderBytes, s) != cudaSuccess) {
-      cudaFreeAsync(ws, s);
-      return PKV_ERR_CUDA;
-    }
   }
-  p.counters = reinterpret_cast<unsigned int*>(ws);
+  p.arrivals = reinterpret_cast<unsigned long long*>(ws);
+  p.arrival = f8_arrival();
   p.unit_recs = reinterpret_cast<float*>(ws + kF8HeaderBytes);
   p.cta_recs = p.unit_recs + static_cast<size_t>(di.sm_count) * f8_warps(p.rows <= 8 ? 1 : 2) * p.rec_floats;
   st = dtype == PKV_BF16 ? dispatch_decode_f8<true>(head_dim, map, p, di, s)

@@ -53,7 +53,7 @@ __host__ __device__ constexpr int f8_seg_slots(int NR) { return NR == 1 ? 2 : 7;
 // 12 warps, 57.6 with 16; 4 x 131072: 186, 178.  16 rows, 32 x 4 queries: 42.1 with
 // 8, 44.9 with 12.
 constexpr int kF8W1 = 16, kF8W2 = 8;
-constexpr int kF8HeaderBytes = 4096;                  // workspace: a counter per CTA
+constexpr int kF8HeaderBytes = 4096;                  // workspace: the arrivals at each CTA's segment, 8 bytes
 constexpr float kF8RefBelow = 7.f, kF8RefSlack = 14.f;
 
 struct DecodeF8Params {
@@ -62,7 +62,12 @@ struct DecodeF8Params {
   const float2* scales;  // [num_blocks][n_kv]
   const int32_t* block_tables;
   const int32_t* context_lens;
-  unsigned int* counters;  // [CTAs], 0 between launches
+  // [CTAs]: the CTAs done with the segment that starts in that one and goes on behind
+  // it.  Each adds `arrival`: 1 in the bits from 48 on, below them a number that differs
+  // from call to call, so that a word the workspace held before is told from arrivals
+  // (f8_settle).  0 again after a launch.
+  unsigned long long* arrivals;
+  unsigned long long arrival;
   float* unit_recs;        // [units][rec_floats]: a segment that ends inside a unit and began before it
   float* cta_recs;         // [CTAs][2][rec_floats]: the CTA's share of a segment from before it, of one that goes on
   int32_t max_blocks_per_seq, batch, num_blocks, n_q_heads, n_kv_heads, q_len;
@@ -111,11 +116,32 @@ __device__ __forceinline__ void ldsm_b8_x2_trans(uint32_t addr, uint32_t& r0, ui
                : "r"(addr));
 }
 
-// Adds 1, ordered on both sides at gpu scope (for the CTA, between two of its barriers).
-__device__ __forceinline__ unsigned int add_acq_rel(unsigned int* at) {
-  unsigned int r;
-  asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(r) : "l"(at) : "memory");
+// Adds `x`, ordered on both sides at gpu scope (for the CTA, between two of its barriers).
+__device__ __forceinline__ unsigned long long add_acq_rel(unsigned long long* at, unsigned long long x) {
+  unsigned long long r;
+  asm volatile("atom.add.acq_rel.gpu.global.u64 %0, [%1], %2;" : "=l"(r) : "l"(at), "l"(x) : "memory");
   return r;
+}
+
+__device__ __forceinline__ unsigned long long load_relaxed(const unsigned long long* at) {
+  unsigned long long r;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(r) : "l"(at) : "memory");
+  return r;
+}
+
+// Sets a word of the arrivals to 0 unless it holds some of this call's n already
+// (j `arrival`, j < n).  `word` is what it held when it was read last.  Every CTA does
+// this in front of its own arrival, so that none is counted on top of, or lost with,
+// what was there before the call: a workspace needs no clearing.
+__device__ __forceinline__ void f8_settle(unsigned long long* at, unsigned long long word, unsigned long long arrival,
+                                          int n) {
+  while (true) {
+    const unsigned long long j = word >> 48;
+    if (j < static_cast<unsigned long long>(n) && word == j * arrival) return;
+    const unsigned long long now = atomicCAS(at, word, 0ull);
+    if (now == word) return;
+    word = now;  // another CTA of the call has settled it, or arrived
+  }
 }
 
 // 8 x 8 transpose of packed 16-bit pairs: lane (g, t) holds row g, columns 2 t, 2 t + 1 before and after.
@@ -927,6 +953,13 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   // Four rows a warp.  (A row a warp, its pieces shared by the groups of lanes:
   // 59 us against 43 for 32 x 4 queries, no gain where there are few rows.)
   const int items = (p.rows + 3) / 4;
+  // The first group may come from before the CTA, the last may go on behind it (one may do both).
+  const bool from_before = ng > 0 && groups[0].st < A;
+  const bool goes_on = ng > 0 && groups[ng - 1].en > E && groups[ng - 1].st >= A;
+  const bool arrives = threadIdx.x == 0 ? from_before : threadIdx.x == 1 && goes_on;
+  const F8Group& shared_seg = groups[threadIdx.x == 0 || ng == 0 ? 0 : ng - 1];
+  unsigned long long word = 0;  // on its way during the merges
+  if (arrives) word = load_relaxed(p.arrivals + shared_seg.c0);
   for (int i = warp; i < ng * items; i += W) {
     const F8Group& gr = groups[i / items];
     F8Pieces pc;  // in the rings; the last one in its unit's record if more follows it there
@@ -944,21 +977,17 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   }
 
   // ---------------- segments shared with other CTAs ----------------
-  // The first group may come from before the CTA, the last may go on behind it (one may do both).
-  const bool from_before = ng > 0 && groups[0].st < A;
-  const bool goes_on = ng > 0 && groups[ng - 1].en > E && groups[ng - 1].st >= A;
   if (!from_before && !goes_on) return;
   __syncthreads();
   if (threadIdx.x < 2) {
     int fin = 0;
-    if (threadIdx.x == 0 ? from_before : goes_on) {
-      const F8Group& gr = groups[threadIdx.x == 0 ? 0 : ng - 1];
-      const unsigned int n = static_cast<unsigned int>(gr.n_ctas);
-      const unsigned int before = add_acq_rel(p.counters + gr.c0);  // after every record of this CTA, before any it reads
-      if (before >= n) flag_error(PKV_DEVERR_SCHEDULE);
-      if (before + 1 >= n) {
+    if (arrives) {
+      unsigned long long* at = p.arrivals + shared_seg.c0;
+      f8_settle(at, word, p.arrival, shared_seg.n_ctas);
+      const unsigned long long before = add_acq_rel(at, p.arrival);  // after every record of this CTA, before any it reads
+      if (before == static_cast<unsigned long long>(shared_seg.n_ctas - 1) * p.arrival) {
         fin = 1;
-        p.counters[gr.c0] = 0;
+        *at = 0;
       }
     }
     last_of[threadIdx.x] = fin;

@@ -377,6 +377,37 @@ def test_decode_refuses_a_workspace_that_does_not_fit():
         run_decode(case, workspace=torch.zeros(need, dtype=torch.uint8))
 
 
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_workspace_may_hold_anything(captured):
+    """Words that look like few, many or all arrivals, and floats, in front of every call."""
+    cases = [decode_case([20000], 4, 1, 128, torch.bfloat16, seed=62),
+             decode_case([3000, 70, 900, 1, 2222], 16, 4, 128, torch.float16, seed=63),
+             decode_case([500, 1300, 40], 4, 2, 64, torch.bfloat16, seed=64, q_len=3)]
+    for case in cases:
+        want = check_decode(case)
+        args = [case[0].cuda(), case[1], case[2], case[3].cuda(), case[4].cuda(), case[5]]
+        q_len = case[0].shape[1] if case[0].dim() == 4 else 1
+        need = pkv.paged_attention_fp8_workspace_size(len(case[4]), q_len, case[0].shape[-2], case[1].shape[1],
+                                                      case[0].shape[-1])
+        ws, out = torch.zeros(need // 8, dtype=torch.int64, device="cuda"), torch.empty_like(args[0])
+        run = lambda: pkv.paged_attention_decode_fp8(*args, out=out, workspace=ws)  # noqa: E731
+        if captured:
+            graph = torch.cuda.CUDAGraph()
+            with torch.cuda.graph(graph):
+                run()
+            run = graph.replay
+        for fill in (1, 2, 7, 147, 148, 1 << 32, 1 << 48, 5 << 48, (1 << 48) + 1, -1, 0x7F7F7F7F7F7F7F7F, 0x3F80000040400000):
+            ws.fill_(fill)
+            run()
+            assert torch.equal(bits(out.cpu()), bits(want))
+            run()  # what a call leaves behind serves the next one
+            assert torch.equal(bits(out.cpu()), bits(want))
+            ws.random_()
+            run()
+            assert torch.equal(bits(out.cpu()), bits(want))
+    assert pkv.pkv_get_device_error() == 0
+
+
 def test_two_graphs_share_a_workspace_in_turn():
     cases = [decode_case([2500, 40], 8, 2, 128, torch.bfloat16, seed=47), decode_case([300] * 9, 16, 1, 64, torch.float16, seed=48)]
     want = [run_decode(c) for c in cases]
