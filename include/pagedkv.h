@@ -579,7 +579,8 @@ pkv_status paged_kv_append_rope(const void* q, int64_t q_stride, const void* k, 
  * tokens away (tokens not of this call become 0).  A block fills from offset 0
  * on, so nothing that lives is lost; rewriting offset 0 of a block in use
  * does lose the block's other tokens.
- * Slots as paged_kv_append (a negative one is padding).  The tokens of one
+ * Slots as paged_kv_append (a negative one is padding; one beyond the pool is
+ * left out, wherever it stands).  The tokens of one
  * block have to be consecutive in the call, in any order, with no padding
  * between them (a step's one token per sequence and a prompt's tokens in order
  * are); of two with the same slot the last counts.  A block whose tokens come

@@ -479,10 +479,11 @@ __device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t b
   for (int base = first;; base += 32) {
     int64_t s = -1;
     if (base + lane < rp.num_tokens) s = __ldg(rp.slot_mapping + base + lane);
-    const uint32_t other = __ballot_sync(0xffffffffu, s < 0 || (s >> 4) != blk);
+    // A slot beyond the pool is skipped where it stands, in the middle of a run too.
+    const uint32_t other = __ballot_sync(0xffffffffu, s < 0 || (s < rp.num_slots && (s >> 4) != blk));
     const int n = other ? __ffs(other) - 1 : 32;
     int off = -1;
-    if (lane < n) {
+    if (lane < n && s < rp.num_slots) {
       off = static_cast<int>(s & 15);
       if constexpr (kRope) {
         const int64_t pos = __ldg(rp.rope.positions + base + lane);
@@ -541,16 +542,24 @@ __global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_f8_kernel(
   const int kind_begin = one_kind ? item & 1 : 0, kind_end = one_kind ? kind_begin + 1 : 2;
   // Lane l looks at token l - 1 of the chunk, so that lane 0 holds the token before it.
   const int64_t t = chunk * p.tokens_per_pair + lane - 1;
+  constexpr int64_t kBeyond = -2;  // a slot beyond the pool, as if its token were not there
   int64_t blk = -1;
   if (t >= 0 && t < rp.num_tokens && lane <= p.tokens_per_pair) {
     const int64_t s = __ldg(rp.slot_mapping + t);
     if (s >= rp.num_slots) {
       if (item == 0 && lane > 0) flag_error(PKV_DEVERR_SLOT);
+      blk = kBeyond;
     } else if (s >= 0) {
       blk = s >> 4;
     }
   }
-  const int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
+  int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
+  if (lane > 0 && blk >= 0) {
+    for (int64_t u = t - 1; before == kBeyond; --u) {  // u: the last token looked at
+      const int64_t s = u > 0 ? __ldg(rp.slot_mapping + u - 1) : -1;
+      before = s >= rp.num_slots ? kBeyond : s >= 0 ? s >> 4 : -1;
+    }
+  }
   uint32_t starts = __ballot_sync(0xffffffffu, lane > 0 && blk >= 0 && blk != before);
   while (starts) {
     const int l = __ffs(starts) - 1;

@@ -143,6 +143,35 @@ def test_append_leaves_out_bad_slots_and_positions():
     same_cache(kv, scales, values, want)
 
 
+@pytest.mark.parametrize("many", [False, True])  # a token or sixteen to each pair of warps
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("first,count", [(0, 1), (3, 1), (14, 1), (15, 2), (16, 3), (1, 17), (5, 40), (30, 70)])
+def test_append_slots_beyond_the_pool_inside_a_block(first, count, rotated, many):
+    """`count` bad slots at every place `first` of a stretch: the block's tokens on both sides are one run."""
+    g = torch.Generator().manual_seed(first + count)
+    n_kv, blocks = (40, 12) if many else (2, 12)
+    pos = torch.arange(5, 5 + 70)
+    slots = torch.randperm(blocks, generator=g)[pos // 16] * 16 + pos % 16
+    bad = blocks * 16 + torch.randint(0, 1 << 40, (count,), generator=g)
+    slots = torch.cat((slots[:first], bad, slots[first:], bad[:1]))
+    n = len(slots)
+    assert (n * n_kv > 16 * torch.cuda.get_device_properties(0).multi_processor_count) == many
+    size = torch.exp2(torch.randint(-6, 7, (n, 1, 1), generator=g).float())
+    k, v = (torch.randn((n, n_kv, 64), generator=g) * size for _ in range(2))
+    kv, scales = random_cache(blocks, n_kv, 64, first)
+    values, want = host(kv, scales)
+    kf = k
+    if rotated:
+        table, at = pkv.rotary_table(128, 64, device="cpu"), torch.randint(0, 128, (n,), generator=g)
+        kf = ref.rotate32(k, table, at, False)
+        pkv.paged_kv_append_rope_fp8(k.cuda(), v.cuda(), at.cuda(), table.cuda(), slots.cuda(), kv, scales)
+    else:
+        pkv.paged_kv_append_fp8(k.cuda(), v.cuda(), slots.cuda(), kv, scales)
+    assert pkv.pkv_get_device_error() == pkv.DEVERR_SLOT
+    ref.append(values, want, kf, v, slots, blocks)
+    same_cache(kv, scales, values, want)
+
+
 def test_append_long_prompts_and_one_token_warps_agree():
     """More tokens than one warp each can hold: the other split of the call into warps."""
     g = torch.Generator().manual_seed(15)
