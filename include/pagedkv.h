@@ -623,6 +623,8 @@ pkv_status paged_kv_copy_blocks_fp8(uint8_t* kv_cache, float* kv_scales, const i
  *               device, 256-byte aligned, for one call at a time.  It may hold
  *               anything (no clearing, no state from call to call) and serves
  *               calls of any sizes that fit it; NULL allocates it on `stream`.
+ *               The size for a q_len and head counts serves every smaller q_len
+ *               and every smaller n_q_heads / n_kv_heads, and any batch.
  * A block id or a context length out of range is treated as in
  * paged_attention_decode_mq.  A NaN in a key or value reaches the rows that see
  * its token, and no others.

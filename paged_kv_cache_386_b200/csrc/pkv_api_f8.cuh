@@ -278,9 +278,16 @@ pkv_status paged_attention_fp8_workspace_size(int32_t batch, int32_t q_len, int3
   if (q_len > 16 || batch > PKV_MAX_BATCH || (head_dim != 64 && head_dim != 128)) return PKV_ERR_UNSUPPORTED;
   DeviceInfo di;
   if (device_info(&di) != PKV_OK) return PKV_ERR_CUDA;
-  int nseg, rows;
-  decode_f8_segments(n_q_heads / n_kv_heads * q_len, &nseg, &rows);
-  *bytes = decode_f8_workspace(di.sm_count, rows, head_dim);
+  // Calls with fewer rows can need more (8 rows: 16 warps a CTA, 9 rows: 8): the
+  // most that any of them does, so that a size serves smaller q_len and groups too.
+  const int64_t total_rows = static_cast<int64_t>(n_q_heads / n_kv_heads) * q_len;
+  *bytes = 0;
+  for (int total = 1; total <= (total_rows < 16 ? static_cast<int>(total_rows) : 16); ++total) {
+    int nseg, rows;
+    decode_f8_segments(total, &nseg, &rows);
+    const size_t need = decode_f8_workspace(di.sm_count, rows, head_dim);
+    if (need > *bytes) *bytes = need;
+  }
   return PKV_OK;
 }
 

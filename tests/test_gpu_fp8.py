@@ -395,6 +395,21 @@ def test_decode_of_the_largest_batch(n_q, n_kv, d, q_len):
     assert ((got[pick].double() - want).abs() <= ref.decode_tolerance(want, bound, q.dtype)).all()
 
 
+@pytest.mark.parametrize("group", [1, 3, 4, 7, 16, 20])
+@pytest.mark.parametrize("d", [64, 128])
+def test_a_workspace_for_the_longest_draft_serves_shorter_ones(group, d):
+    size = lambda g, q_len: pkv.paged_attention_fp8_workspace_size(3, q_len, 2 * g, 2, d)  # noqa: E731
+    sizes = [size(group, q_len) for q_len in range(1, 17)]
+    assert sizes == sorted(sizes)
+    assert all(size(g, q_len) <= sizes[q_len - 1] for g in range(1, group) for q_len in (1, 2, 5, 16))
+    for longest in (1, 3, 5, 16):
+        ws = pkv.new_workspace(sizes[longest - 1])
+        for q_len in range(1, longest + 1):
+            case = decode_case([700, 33, q_len], 2 * group, 2, d, torch.bfloat16, seed=q_len, q_len=q_len)
+            assert torch.equal(bits(run_decode(case, workspace=ws)), bits(run_decode(case)))
+    assert pkv.pkv_get_device_error() == 0
+
+
 def test_decode_refuses_a_workspace_that_does_not_fit():
     case = decode_case([40], 8, 2, 128, torch.bfloat16, seed=46)
     need = pkv.paged_attention_fp8_workspace_size(1, 1, 8, 2, 128)
