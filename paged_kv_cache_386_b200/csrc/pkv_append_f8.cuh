@@ -19,7 +19,9 @@ namespace pkv {
 
 // These kernels are launched while the kernel in front of them on the stream ends
 // (launch_early), and wait here until its writes can be seen, before they read or
-// write any memory but their own shared memory.
+// write any memory but their own shared memory.  Inputs are read by ordinary loads:
+// the read-only path (ld.global.nc) is for memory that nothing writes from a kernel's
+// start on.
 __device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Sixteen elements of a head row as fp32: two pieces of eight consecutive dims.
@@ -97,9 +99,9 @@ __device__ __forceinline__ uint64_t mul_f2(uint64_t a, uint64_t b) {
 // cos and sin of the chunk's eight pairs.
 __device__ __forceinline__ void load_cos_sin(const RopeTable& t, int64_t pos, int c, float (&cs)[8], float (&sn)[8]) {
   const float* row = t.table + pos * t.rot + c * 8;
-  const float4 c0 = __ldg(reinterpret_cast<const float4*>(row)), c1 = __ldg(reinterpret_cast<const float4*>(row) + 1);
+  const float4 c0 = reinterpret_cast<const float4*>(row)[0], c1 = reinterpret_cast<const float4*>(row)[1];
   row += t.rot / 2;
-  const float4 s0 = __ldg(reinterpret_cast<const float4*>(row)), s1 = __ldg(reinterpret_cast<const float4*>(row) + 1);
+  const float4 s0 = reinterpret_cast<const float4*>(row)[0], s1 = reinterpret_cast<const float4*>(row)[1];
   cs[0] = c0.x, cs[1] = c0.y, cs[2] = c0.z, cs[3] = c0.w, cs[4] = c1.x, cs[5] = c1.y, cs[6] = c1.z, cs[7] = c1.w;
   sn[0] = s0.x, sn[1] = s0.y, sn[2] = s0.z, sn[3] = s0.w, sn[4] = s1.x, sn[5] = s1.y, sn[6] = s1.z, sn[7] = s1.w;
 }
@@ -176,14 +178,14 @@ __device__ __forceinline__ void rope_append_item(const RopeAppendParams& p, uint
   const int c = static_cast<int>(item % chunks);
   const int h_begin = head_group * p.heads_per_thread;
   const int h_end = min(n_heads, h_begin + p.heads_per_thread);
-  const int64_t pos = __ldg(p.rope.positions + tok);
+  const int64_t pos = p.rope.positions[tok];
   if (pos < 0 || pos >= p.rope.max_pos) {
     if (c == 0 && h_begin == 0) flag_error(PKV_DEVERR_POSITION);
     return;
   }
   int64_t slot = -1;
   if (h_end > p.n_q) {
-    slot = __ldg(p.slot_mapping + tok);
+    slot = p.slot_mapping[tok];
     if (slot >= p.num_slots) {
       if (c == 0 && h_end == n_heads) flag_error(PKV_DEVERR_SLOT);
       slot = -1;
@@ -364,7 +366,7 @@ __device__ __forceinline__ void append_f8_rows(const AppendF8Params& p, int64_t 
       y[it].widen(v1[it]);
       if (c * 16 < rp.rope.rot && tok[it] >= 0) {
         float cs[8], sn[8];
-        load_cos_sin(rp.rope, __ldg(rp.rope.positions + tok[it]), c, cs, sn);
+        load_cos_sin(rp.rope, rp.rope.positions[tok[it]], c, cs, sn);
         rotate_chunk(v0[it], v1[it], cs, sn, rp.rope.interleaved != 0);
       }
     }
@@ -478,7 +480,7 @@ __device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t b
   int src = -1;
   for (int base = first;; base += 32) {
     int64_t s = -1;
-    if (base + lane < rp.num_tokens) s = __ldg(rp.slot_mapping + base + lane);
+    if (base + lane < rp.num_tokens) s = rp.slot_mapping[base + lane];
     // A slot beyond the pool is skipped where it stands, in the middle of a run too.
     const uint32_t other = __ballot_sync(0xffffffffu, s < 0 || (s < rp.num_slots && (s >> 4) != blk));
     const int n = other ? __ffs(other) - 1 : 32;
@@ -486,7 +488,7 @@ __device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t b
     if (lane < n && s < rp.num_slots) {
       off = static_cast<int>(s & 15);
       if constexpr (kRope) {
-        const int64_t pos = __ldg(rp.rope.positions + base + lane);
+        const int64_t pos = rp.rope.positions[base + lane];
         if (pos < 0 || pos >= rp.rope.max_pos) {  // left out, as if it were padding
           flag_error(PKV_DEVERR_POSITION);
           off = -1;
@@ -545,7 +547,7 @@ __global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_f8_kernel(
   constexpr int64_t kBeyond = -2;  // a slot beyond the pool, as if its token were not there
   int64_t blk = -1;
   if (t >= 0 && t < rp.num_tokens && lane <= p.tokens_per_pair) {
-    const int64_t s = __ldg(rp.slot_mapping + t);
+    const int64_t s = rp.slot_mapping[t];
     if (s >= rp.num_slots) {
       if (item == 0 && lane > 0) flag_error(PKV_DEVERR_SLOT);
       blk = kBeyond;
@@ -556,7 +558,7 @@ __global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_f8_kernel(
   int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
   if (lane > 0 && blk >= 0) {
     for (int64_t u = t - 1; before == kBeyond; --u) {  // u: the last token looked at
-      const int64_t s = u > 0 ? __ldg(rp.slot_mapping + u - 1) : -1;
+      const int64_t s = u > 0 ? rp.slot_mapping[u - 1] : -1;
       before = s >= rp.num_slots ? kBeyond : s >= 0 ? s >> 4 : -1;
     }
   }
@@ -583,7 +585,7 @@ struct CopyF8Params {
 // CTAs stride over the pairs, four 16-byte loads in flight per thread.
 __global__ void __launch_bounds__(256) pkv_copy_blocks_f8_kernel(const CopyF8Params p) {
   for (int pair = blockIdx.x; pair < p.n_pairs; pair += gridDim.x) {
-    const int32_t s = __ldg(p.src + pair), d = __ldg(p.dst + pair);
+    const int32_t s = p.src[pair], d = p.dst[pair];
     if (s < 0 || s >= p.num_blocks || d < 0 || d >= p.num_blocks) {
       if (threadIdx.x == 0) flag_error(PKV_DEVERR_BLOCK_ID);
       continue;

@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     auto slots_of = [&](int c) { return c > 0 ? ((c + kBlockTokens - 1) / kBlockTokens + kSeg) * p.ng : 0; };
     int local = 0;
     for (int b = lo; b < hi; ++b) {
-      const int c0 = __ldg(p.context_lens + b);
+      const int c0 = p.context_lens[b];
       int c = clamp_ctx(c0, max_ctx);
       if (c > 0 && c < p.q_len) c = 0;
       if (c != c0) flag_error(PKV_DEVERR_CONTEXT);
@@ -814,7 +814,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
     int left = k1 - max(k0, wi.st + kSeg);  // slots from tile wi.j on; a tile while positive
     auto table = [&](int b, int j) {
       const int at = j + lane;
-      return at < p.max_blocks_per_seq ? __ldg(p.block_tables + static_cast<size_t>(b) * p.max_blocks_per_seq + at) : -1;
+      return at < p.max_blocks_per_seq ? p.block_tables[static_cast<size_t>(b) * p.max_blocks_per_seq + at] : -1;
     };
     int wb = -1, wj = 0, ids = 0, nxb = -1, nxj = 0, nx_ids = 0;
     auto window = [&]() {
