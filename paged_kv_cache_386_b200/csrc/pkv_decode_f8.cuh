@@ -130,9 +130,9 @@ __device__ __forceinline__ unsigned long long load_relaxed(const unsigned long l
 }
 
 // Sets a word of the arrivals to 0 unless it holds some of this call's n already
-// (j `arrival`, j < n).  `word` is what it held when it was read last.  Every CTA does
-// this in front of its own arrival, so that none is counted on top of, or lost with,
-// what was there before the call: a workspace needs no clearing.
+// (j `arrival`, j < n).  `word` is what it held when last read.  Every CTA does this in front of its own arrival, so that
+// none is counted on top of, or lost with, what was there before the call: a workspace
+// needs no clearing.
 __device__ __forceinline__ void f8_settle(unsigned long long* at, unsigned long long word, unsigned long long arrival,
                                           int n) {
   while (true) {
@@ -956,10 +956,10 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
   // The first group may come from before the CTA, the last may go on behind it (one may do both).
   const bool from_before = ng > 0 && groups[0].st < A;
   const bool goes_on = ng > 0 && groups[ng - 1].en > E && groups[ng - 1].st >= A;
-  const bool arrives = threadIdx.x == 0 ? from_before : threadIdx.x == 1 && goes_on;
-  const F8Group& shared_seg = groups[threadIdx.x == 0 || ng == 0 ? 0 : ng - 1];
-  unsigned long long word = 0;  // on its way during the merges
-  if (arrives) word = load_relaxed(p.arrivals + shared_seg.c0);
+  // Their words are settled beside the merges, by the warp that has the fewest of them.
+  const bool settles = warp == W - 1 && (lane == 0 ? from_before : lane == 1 && goes_on);
+  unsigned long long word = 0;
+  if (settles) word = load_relaxed(p.arrivals + groups[lane == 0 ? 0 : ng - 1].c0);
   for (int i = warp; i < ng * items; i += W) {
     const F8Group& gr = groups[i / items];
     F8Pieces pc;  // in the rings; the last one in its unit's record if more follows it there
@@ -978,14 +978,18 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
 
   // ---------------- segments shared with other CTAs ----------------
   if (!from_before && !goes_on) return;
+  if (settles) {
+    const F8Group& gr = groups[lane == 0 ? 0 : ng - 1];
+    f8_settle(p.arrivals + gr.c0, word, p.arrival, gr.n_ctas);
+  }
   __syncthreads();
   if (threadIdx.x < 2) {
     int fin = 0;
-    if (arrives) {
-      unsigned long long* at = p.arrivals + shared_seg.c0;
-      f8_settle(at, word, p.arrival, shared_seg.n_ctas);
-      const unsigned long long before = add_acq_rel(at, p.arrival);  // after every record of this CTA, before any it reads
-      if (before == static_cast<unsigned long long>(shared_seg.n_ctas - 1) * p.arrival) {
+    if (threadIdx.x == 0 ? from_before : goes_on) {
+      const F8Group& gr = groups[threadIdx.x == 0 ? 0 : ng - 1];
+      unsigned long long* at = p.arrivals + gr.c0;
+      // After every record of this CTA, before any it reads.
+      if (add_acq_rel(at, p.arrival) == static_cast<unsigned long long>(gr.n_ctas - 1) * p.arrival) {
         fin = 1;
         *at = 0;
       }
