@@ -482,10 +482,11 @@ __device__ __forceinline__ void append_f8_run(const AppendF8Params& p, int64_t b
     int64_t s = -1;
     if (base + lane < rp.num_tokens) s = rp.slot_mapping[base + lane];
     // A slot beyond the pool is skipped where it stands, in the middle of a run too.
-    const uint32_t other = __ballot_sync(0xffffffffu, s < 0 || (s < rp.num_slots && (s >> 4) != blk));
+    const bool here = (s >> 4) == blk;
+    const uint32_t other = __ballot_sync(0xffffffffu, !here && s < rp.num_slots);
     const int n = other ? __ffs(other) - 1 : 32;
     int off = -1;
-    if (lane < n && s < rp.num_slots) {
+    if (lane < n && here) {
       off = static_cast<int>(s & 15);
       if constexpr (kRope) {
         const int64_t pos = rp.rope.positions[base + lane];
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(256, DT == kF32 ? 3 : 4) pkv_append_f8_kernel(
     }
   }
   int64_t before = __shfl_up_sync(0xffffffffu, blk, 1);
-  if (lane > 0 && blk >= 0) {
+  if (__any_sync(0xffffffffu, before == kBeyond)) {
     for (int64_t u = t - 1; before == kBeyond; --u) {  // u: the last token looked at
       const int64_t s = u > 0 ? rp.slot_mapping[u - 1] : -1;
       before = s >= rp.num_slots ? kBeyond : s >= 0 ? s >> 4 : -1;
