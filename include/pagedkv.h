@@ -638,6 +638,16 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
                                       int32_t block_size, void* out, pkv_dtype dtype, void* workspace,
                                       size_t workspace_bytes, void* stream);
 
+/* paged_attention_decode_fp8 with options: wait_limit_us and test_withhold_unit
+ * (u + 1: only the first tile is never copied, of the unit that runs the start
+ * of unit u's share), the others zero. */
+pkv_status paged_attention_decode_fp8_ex(const void* q, const uint8_t* kv_cache, const float* kv_scales,
+                                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t* context_lens, int32_t batch, int32_t q_len, int32_t num_blocks,
+                                         float scale, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                         int32_t block_size, void* out, pkv_dtype dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream, const pkv_decode_options* options);
+
 /*
  * pkv_get_device_error -- synchronise `stream`, then read and clear the
  * current device's error word.  *flags receives the PKV_DEVERR_* bits seen

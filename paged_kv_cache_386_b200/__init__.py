@@ -148,6 +148,8 @@ def _load() -> ctypes.CDLL:
     lib.paged_attention_decode_fp8.argtypes = [p, p, p, p, i32, p, i32, i32, i32, f32, i32, i32, i32, i32, p,
                                                ctypes.c_int, p, sz, p]
     lib.paged_attention_decode_fp8.restype = ctypes.c_int
+    lib.paged_attention_decode_fp8_ex.argtypes = lib.paged_attention_decode_fp8.argtypes + [p]
+    lib.paged_attention_decode_fp8_ex.restype = ctypes.c_int
     for name, args in (("pkv_bm_create", [i32, i32, i32, ctypes.POINTER(p)]),
                        ("pkv_bm_hash_blocks", [p, i64, i32, u64, p]),
                        ("pkv_bm_add_sequence", [p, i64, i64, p, ctypes.POINTER(i64)]),
@@ -643,16 +645,16 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _launch(entry: str, index: int, stream, *args) -> None:
-    """Calls C entry point `entry`, whose last argument is the stream, on device `index`."""
+def _launch(entry: str, index: int, stream, *args, after=()) -> None:
+    """Calls C entry point `entry` with `args`, the stream and `after`, on device `index`."""
     fn = getattr(_lib or _load(), entry)
     if stream is not None:
         raw = _stream(stream)
     if torch.cuda.current_device() == index:
-        status = fn(*args, _raw_stream(index) if stream is None else raw)
+        status = fn(*args, _raw_stream(index) if stream is None else raw, *after)
     else:
         with torch.cuda.device(index):
-            status = fn(*args, _raw_stream(index) if stream is None else raw)
+            status = fn(*args, _raw_stream(index) if stream is None else raw, *after)
     if status != PKV_OK:
         raise PagedKVError(status, entry)
 
@@ -832,13 +834,17 @@ def paged_attention_fp8_workspace_size(batch: int, q_len: int, n_q_heads: int, n
 
 
 def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_lens, scale: float, out=None,
-                               workspace=None, block_size: int = 16, stream=None):
+                               workspace=None, block_size: int = 16, stream=None, wait_limit_us: int = 0,
+                               test_withhold_unit: int = -1):
     """paged_attention_decode over the FP8 cache.  ``q`` is ``[batch, n_q, d]``,
     or ``[batch, q_len, n_q, d]`` for several queries per sequence (query i sees
     its context up to position ``ctx - q_len + i``), float16 or bfloat16.
     ``workspace``: paged_attention_fp8_workspace_size bytes (of any contents),
-    for one call at a time.  Returns ``out`` (shape and dtype of q)."""
-    if stream is None and block_size == 16 and (quick := _ext or _quick()):
+    for one call at a time.  ``wait_limit_us`` and ``test_withhold_unit`` are
+    the failure-path test hooks of paged_attention_decode.  Returns ``out``
+    (shape and dtype of q)."""
+    hooked = wait_limit_us != 0 or test_withhold_unit != -1
+    if stream is None and block_size == 16 and not hooked and (quick := _ext or _quick()):
         done = quick.decode_fp8(q, kv_cache, kv_scales, block_tables, context_lens, scale, out, workspace)
         if done is not NotImplemented:
             return done
@@ -865,8 +871,9 @@ def paged_attention_decode_fp8(q, kv_cache, kv_scales, block_tables, context_len
     ws_ptr, ws_bytes = None, 0
     if workspace is not None:
         ws_ptr, ws_bytes = _flat(workspace, "workspace"), workspace.numel() * workspace.element_size()
-    _launch("paged_attention_decode_fp8", index, stream, _flat(q, "q"), _flat(kv_cache, "kv_cache"),
+    opts = _Options(wait_limit_us=int(wait_limit_us), test_withhold_unit=int(test_withhold_unit) + 1) if hooked else None
+    _launch("paged_attention_decode_fp8_ex", index, stream, _flat(q, "q"), _flat(kv_cache, "kv_cache"),
             _flat(kv_scales, "kv_scales"), _flat(block_tables, "block_tables"), block_tables.shape[1],
             _flat(context_lens, "context_lens"), B, q_len, num_blocks, float(scale), n_q, n_kv, d, block_size, out.data_ptr(),
-            _DTYPE[q.dtype], ws_ptr, ws_bytes)
+            _DTYPE[q.dtype], ws_ptr, ws_bytes, after=(ctypes.byref(opts) if hooked else None,))
     return out

@@ -297,11 +297,27 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
                                       float scale, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
                                       int32_t block_size, void* out, pkv_dtype dtype, void* workspace,
                                       size_t workspace_bytes, void* stream) {
+  return paged_attention_decode_fp8_ex(q, kv_cache, kv_scales, block_tables, max_blocks_per_seq, context_lens, batch,
+                                       q_len, num_blocks, scale, n_q_heads, n_kv_heads, head_dim, block_size, out,
+                                       dtype, workspace, workspace_bytes, stream, nullptr);
+}
+
+pkv_status paged_attention_decode_fp8_ex(const void* q, const uint8_t* kv_cache, const float* kv_scales,
+                                         const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                         const int32_t* context_lens, int32_t batch, int32_t q_len, int32_t num_blocks,
+                                         float scale, int32_t n_q_heads, int32_t n_kv_heads, int32_t head_dim,
+                                         int32_t block_size, void* out, pkv_dtype dtype, void* workspace,
+                                         size_t workspace_bytes, void* stream, const pkv_decode_options* options) {
   pkv_status st = check_decode_args(q, kv_cache, kv_cache, block_tables, max_blocks_per_seq, context_lens, batch,
                                     num_blocks, scale, n_q_heads, n_kv_heads, head_dim, block_size, out, dtype);
   if (st != PKV_OK) return st;
   if (q_len < 1) return PKV_ERR_INVALID_ARG;
   if (q_len > 16 || dtype == PKV_F32) return PKV_ERR_UNSUPPORTED;
+  pkv_decode_options opt = {};
+  if (options) opt = *options;
+  if (opt.num_units || opt.force_simt || opt.balance_chunks || opt.static_permille || opt.wait_limit_us < 0 ||
+      opt.test_withhold_unit < 0 || opt.reserved[0] || opt.reserved[1])
+    return PKV_ERR_INVALID_ARG;
   if (batch == 0) return PKV_OK;
   if (!kv_scales || (reinterpret_cast<uintptr_t>(kv_scales) & 7u)) return PKV_ERR_INVALID_ARG;
   if (static_cast<int64_t>(num_blocks) * n_kv_heads > INT32_MAX) return PKV_ERR_UNSUPPORTED;  // a TMA coordinate
@@ -327,7 +343,8 @@ pkv_status paged_attention_decode_fp8(const void* q, const uint8_t* kv_cache, co
   if (static_cast<int64_t>(batch) * (max_blocks_per_seq + f8_seg_slots(2)) * p.ng > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   p.rec_floats = p.rows * (head_dim + 4);
   p.scale_log2 = scale * 1.4426950408889634f;
-  p.wait_limit_ns = kWaitLimitNs;
+  p.wait_limit_ns = opt.wait_limit_us > 0 ? static_cast<uint64_t>(opt.wait_limit_us) * 1000u : kWaitLimitNs;
+  p.withhold_unit = opt.test_withhold_unit - 1;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const size_t need = decode_f8_workspace(di.sm_count, p.rows, head_dim);

@@ -78,6 +78,9 @@ struct DecodeF8Params {
   int32_t ng;          // segments of a sequence, n_kv * nseg
   int32_t rec_floats;  // rows * (D + 4)
   float scale_log2;
+  // Test hook: the first tile is never copied of the unit that runs the start of this
+  // one's share (itself, or the next one where its range is empty); -1: none.
+  int32_t withhold_unit;
   uint64_t wait_limit_ns;
 };
 
@@ -852,13 +855,15 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
       }
     };
     // The next tiles into n slots from `slot` on, a lane for each.
+    const int withhold_at = unit_begin(sc, p.withhold_unit);
+    const int withheld = withhold_at >= k0 && withhold_at < k1 ? 0 : -1;  // which of the unit's tiles
     int issued = 0;
     auto issue = [&](int slot, int n) {
       while (n > 0 && left > 0) {
         window();
         const int off = wi.j - wj, k = min(min(n, left), min(wi.nb - wi.j, 32 - off));
         const int phys = __shfl_sync(0xffffffffu, ids, off + lane);
-        if (lane < k) copy(phys, slot + lane < slot_end ? slot + lane : slot + lane - S);
+        if (lane < k && issued + lane != withheld) copy(phys, slot + lane < slot_end ? slot + lane : slot + lane - S);
         slot += k;
         if (slot >= slot_end) slot -= S;
         n -= k;

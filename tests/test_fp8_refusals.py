@@ -85,6 +85,22 @@ def test_decode(lib, bad, status):
     assert decode(lib, **bad) == status
 
 
+@pytest.mark.parametrize("bad", [dict(num_units=1), dict(force_simt=1), dict(balance_chunks=1), dict(static_permille=800),
+                                 dict(wait_limit_us=-1), dict(test_withhold_unit=-1), dict(reserved=1)])
+def test_decode_options(lib, bad):
+    opts = pkv._Options()
+    for name, value in bad.items():
+        if name == "reserved":
+            opts.reserved[1] = value
+        else:
+            setattr(opts, name, value)
+    f = lib.paged_attention_decode_fp8_ex
+    for batch in (2, 0):
+        assert f(P, P, P, P, 4, P, batch, 1, 8, 0.1, 8, 2, 128, 16, P, 2, None, 0, None, ctypes.byref(opts)) == INVALID
+    assert f(P, P, P, P, 4, P, 0, 1, 8, 0.1, 8, 2, 128, 16, P, 2, None, 0, None, ctypes.byref(pkv._Options(wait_limit_us=5))) == 0
+    assert f(P, P, P, P, 4, P, 0, 1, 8, 0.1, 8, 2, 128, 16, P, 2, None, 0, None, None) == 0
+
+
 def test_decode_of_no_sequence_and_workspace_size(lib):
     assert decode(lib, b=0) == 0
     n = ctypes.c_size_t()

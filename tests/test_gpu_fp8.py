@@ -452,6 +452,27 @@ def test_a_workspace_may_hold_anything(captured):
     assert pkv.pkv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("lens,n_q,n_kv,d,q_len,unit", [
+    ([20000], 4, 1, 128, 1, 40),                 # in the middle of a context that many CTAs share
+    ([3000, 70, 900, 1, 2222], 16, 4, 128, 1, 0),
+    ([3000, 70, 900, 33, 2222], 16, 4, 128, 4, 3),   # 16 rows
+    ([900] * 40, 6, 2, 64, 1, 500),
+])
+@pytest.mark.parametrize("own_workspace", [False, True])
+def test_decode_wait_that_runs_out_and_the_next_call(lens, n_q, n_kv, d, q_len, unit, own_workspace):
+    """A tile that is never copied, others of the unit in flight behind it: the launch ends with
+    the flag, and what it leaves in the workspace does not disturb the next one."""
+    case = decode_case(lens, n_q, n_kv, d, torch.bfloat16, seed=65, q_len=q_len)
+    want = check_decode(case)
+    ws = None if own_workspace else pkv.new_workspace(pkv.paged_attention_fp8_workspace_size(len(lens), q_len, n_q, n_kv, d))
+    for _ in range(2):
+        run_decode(case, workspace=ws, wait_limit_us=5000, test_withhold_unit=unit)
+        assert pkv.pkv_get_device_error() == pkv.DEVERR_TIMEOUT
+        assert torch.equal(bits(run_decode(case, workspace=ws)), bits(want))
+        assert torch.equal(bits(run_decode(case, workspace=ws, wait_limit_us=1_000_000)), bits(want))
+    assert pkv.pkv_get_device_error() == 0
+
+
 def test_two_graphs_share_a_workspace_in_turn():
     cases = [decode_case([2500, 40], 8, 2, 128, torch.bfloat16, seed=47), decode_case([300] * 9, 16, 1, 64, torch.float16, seed=48)]
     want = [run_decode(c) for c in cases]
