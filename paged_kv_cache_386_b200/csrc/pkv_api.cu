@@ -20,6 +20,13 @@ namespace {
 constexpr int kMaxDevices = 64;
 constexpr int32_t kVersion = 10000;  // 1.0.0
 
+// What a failed call of the runtime leaves behind for cudaGetLastError is taken
+// away, or the next entry point that asks for it would report it as its own.
+pkv_status cuda_failed() {
+  (void)cudaGetLastError();
+  return PKV_ERR_CUDA;
+}
+
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -283,7 +290,7 @@ pkv_status launch_decode(const CUtensorMap& mk, const CUtensorMap& mv, const Dec
   attr[0].val.cooperative = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, mk, mv, p) != cudaSuccess) return PKV_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, kern, mk, mv, p) != cudaSuccess) return cuda_failed();
   return cudaGetLastError() == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
@@ -447,7 +454,7 @@ pkv_status launch_prefix_tc(const CUtensorMap& mk, const CUtensorMap& mv, const 
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t cfg = prefix_tc_config(pp, n_kv, splits, stream, &attr);
   if (cfg.gridDim.x > 0x7fffffffu / 2) return PKV_ERR_INVALID_ARG;
-  return cudaLaunchKernelEx(&cfg, kern, mk, mv, pp) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, kern, mk, mv, pp) == cudaSuccess ? PKV_OK : cuda_failed();
 }
 
 }  // namespace
@@ -679,11 +686,11 @@ pkv_status decode_impl(const void* q, const void* k_cache, const void* v_cache, 
   void* ws = workspace;
   bool own = false;
   if (ws == nullptr) {
-    if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return PKV_ERR_CUDA;
+    if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return cuda_failed();
     own = true;
     if (cudaMemsetAsync(ws, 0, kSchedBytes, s) != cudaSuccess) {
       cudaFreeAsync(ws, s);
-      return PKV_ERR_CUDA;
+      return cuda_failed();
     }
   } else if (workspace_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) {
     return PKV_ERR_WORKSPACE;
@@ -742,7 +749,10 @@ pkv_status decode_impl(const void* q, const void* k_cache, const void* v_cache, 
       default: st = dispatch_dim<kBF16>(head_dim, gpad, mk, mv, p, grid, smem, s); break;
     }
   }
-  if (own && cudaFreeAsync(ws, s) != cudaSuccess && st == PKV_OK) st = PKV_ERR_CUDA;
+  if (own && cudaFreeAsync(ws, s) != cudaSuccess) {
+    const pkv_status failed = cuda_failed();
+    if (st == PKV_OK) st = failed;
+  }
   return st;
 }
 }  // namespace
@@ -938,12 +948,12 @@ pkv_status paged_attention_decode_cascade_ex(const void* q, const void* k_cache,
   bool own = false;
   const size_t init_bytes = prefix_init_bytes(batch, n_q_heads, head_dim);
   if (ws == nullptr) {
-    if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return PKV_ERR_CUDA;
+    if (cudaMallocAsync(&ws, need, s) != cudaSuccess) return cuda_failed();
     own = true;
     // The decode part's scheduling counter starts at zero.
     if (cudaMemsetAsync(static_cast<uint8_t*>(ws) + init_bytes, 0, kSchedBytes, s) != cudaSuccess) {
       cudaFreeAsync(ws, s);
-      return PKV_ERR_CUDA;
+      return cuda_failed();
     }
   } else if (workspace_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 255u)) {
     return PKV_ERR_WORKSPACE;
@@ -996,7 +1006,10 @@ pkv_status paged_attention_decode_cascade_ex(const void* q, const void* k_cache,
     st = decode_impl(q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, batch, num_blocks, scale,
                      n_q_heads, n_kv_heads, head_dim, block_size, out, dtype, static_cast<uint8_t*>(ws) + init_bytes,
                      need - init_bytes, stream, nullptr, init, seq_group, n_groups);
-  if (own && cudaFreeAsync(ws, s) != cudaSuccess && st == PKV_OK) st = PKV_ERR_CUDA;
+  if (own && cudaFreeAsync(ws, s) != cudaSuccess) {
+    const pkv_status failed = cuda_failed();
+    if (st == PKV_OK) st = failed;
+  }
   return st;
 }
 

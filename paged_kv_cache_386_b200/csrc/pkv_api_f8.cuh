@@ -80,7 +80,7 @@ pkv_status launch_early(void (*kern)(P...), dim3 grid, int threads, size_t smem,
   a[0].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = a;
   c.numAttrs = 1;
-  return cudaLaunchKernelEx(&c, kern, p...) == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  return cudaLaunchKernelEx(&c, kern, p...) == cudaSuccess ? PKV_OK : cuda_failed();
 }
 
 template <int DT>
@@ -165,7 +165,7 @@ pkv_status launch_decode_f8(const CUtensorMap& map, DecodeF8Params p, const Devi
   if (!opted_in[dev]) {
     if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess || fa.sharedSizeBytes > kStatic ||
         cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, di.smem_optin - kStatic) != cudaSuccess)
-      return PKV_ERR_CUDA;
+      return cuda_failed();
     opted_in[dev] = true;
   }
   const size_t smem = f8_smem_bytes(D, NR, p.rows, p.batch);
@@ -356,7 +356,7 @@ pkv_status paged_attention_decode_fp8_ex(const void* q, const uint8_t* kv_cache,
   const bool own = ws == nullptr;
   if (own) {
     void* at = nullptr;
-    if (cudaMallocAsync(&at, need, s) != cudaSuccess) return PKV_ERR_CUDA;
+    if (cudaMallocAsync(&at, need, s) != cudaSuccess) return cuda_failed();
     ws = static_cast<uint8_t*>(at);
   }
   p.arrivals = reinterpret_cast<unsigned long long*>(ws);
@@ -365,7 +365,10 @@ pkv_status paged_attention_decode_fp8_ex(const void* q, const uint8_t* kv_cache,
   p.cta_recs = p.unit_recs + static_cast<size_t>(di.sm_count) * f8_warps(p.rows <= 8 ? 1 : 2) * p.rec_floats;
   st = dtype == PKV_BF16 ? dispatch_decode_f8<true>(head_dim, map, p, di, s)
                          : dispatch_decode_f8<false>(head_dim, map, p, di, s);
-  if (own && cudaFreeAsync(ws, s) != cudaSuccess && st == PKV_OK) st = PKV_ERR_CUDA;
+  if (own && cudaFreeAsync(ws, s) != cudaSuccess) {
+    const pkv_status failed = cuda_failed();
+    if (st == PKV_OK) st = failed;
+  }
   return st;
 }
 

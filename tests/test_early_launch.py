@@ -2,6 +2,7 @@
 rotating append, the FP8 append and the FP8 decode): whatever that kernel still
 writes is read after it."""
 
+import ctypes
 import re
 
 import pytest
@@ -104,4 +105,49 @@ def test_an_input_that_the_kernel_in_front_writes_last(call, late, captured):
         torch.cuda.synchronize()
         for x, y in zip(got, want, strict=True):
             assert torch.equal(x, y)
+    assert pkv.pkv_get_device_error() == 0
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("call", ["append_rope", "append_fp8", "append_rope_fp8", "decode", "decode_workspace", "decode_16"])
+def test_a_launch_that_fails_is_that_calls_error_alone(call):
+    """A call on a stream whose capture was given up fails; the next call, elsewhere, does not."""
+    rt = ctypes.CDLL("libcudart.so.12")
+    t = Inputs().copies()
+    fp8, q_out = t["codes"].view(torch.float8_e4m3fn), torch.empty_like(t["q"])
+    ws = None
+    if call == "decode_workspace":
+        ws = pkv.new_workspace(pkv.paged_attention_fp8_workspace_size(3, 1, 8, 2, 128))
+    elif call == "decode_16":
+        ws = pkv.new_workspace(pkv.paged_attention_workspace_size(3, 8, 2, 128, torch.bfloat16))
+    calls = {
+        "append_rope": lambda s: pkv.paged_kv_append_rope(t["k"], t["v"], t["pos"], t["table"], t["slots"], t["kc"], t["vc"],
+                                                          q=t["q"], q_out=q_out, stream=s),
+        "append_fp8": lambda s: pkv.paged_kv_append_fp8(t["k"], t["v"], t["slots"], fp8, t["scales"], stream=s),
+        "append_rope_fp8": lambda s: pkv.paged_kv_append_rope_fp8(t["k"], t["v"], t["pos"], t["table"], t["slots"], fp8,
+                                                                  t["scales"], q=t["q"], q_out=q_out, stream=s),
+        "decode": lambda s: pkv.paged_attention_decode_fp8(t["q"], fp8, t["scales"], t["tables"], t["lens"], 0.1, out=q_out,
+                                                           workspace=ws, stream=s),
+        "decode_16": lambda s: pkv.paged_attention_decode(t["q"], t["kc"], t["vc"], t["tables"], t["lens"], 0.1, out=q_out,
+                                                          workspace=ws, stream=s)}
+    calls["decode_workspace"] = calls["decode"]
+    calls[call](None)
+    src, dst = (torch.tensor([i], dtype=torch.int32).cuda() for i in (1, 2))
+    torch.cuda.synchronize()
+    stream, graph = ctypes.c_void_p(), ctypes.c_void_p()
+    assert rt.cudaStreamCreateWithFlags(ctypes.byref(stream), 1) == 0
+    try:
+        assert rt.cudaStreamBeginCapture(stream, 2) == 0  # relaxed: nothing else is held back
+        assert rt.cudaStreamSynchronize(stream) != 0      # not allowed in a capture, which ends it
+        with pytest.raises(pkv.PagedKVError) as e:
+            calls[call](stream.value)
+        assert e.value.status == 4
+    finally:
+        rt.cudaStreamEndCapture(stream, ctypes.byref(graph))
+        rt.cudaStreamDestroy(stream)
+        rt.cudaGetLastError()
+    pkv.paged_kv_copy_blocks_fp8(fp8, t["scales"], src, dst)
+    pkv.paged_kv_append(t["k"], t["v"], t["slots"], t["kc"], t["vc"])
+    calls[call](None)
+    torch.cuda.synchronize()
     assert pkv.pkv_get_device_error() == 0
