@@ -626,18 +626,23 @@ _ext = None
 
 
 def _quick():
-    """The extension, bound to the library; False if it is not built."""
+    """The extension, bound to the library; False if it is not built, or against another torch."""
     global _ext
     if _ext is None:
         lib = _load()
+        from .build import binding_tag
+
         try:
-            from ._binding import append_fp8, append_rope, bind, decode_fp8
+            from . import _binding
         except ImportError:
+            _binding = None
+        if getattr(_binding, "built_for", None) != binding_tag():
             _ext = False
             return False
-        bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+        _binding.bind(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
             "paged_kv_append_rope", "paged_kv_append_rope_fp8", "paged_kv_append_fp8", "paged_attention_decode_fp8")))
-        _ext = SimpleNamespace(append_rope=append_rope, append_fp8=append_fp8, decode_fp8=decode_fp8)
+        _ext = SimpleNamespace(append_rope=_binding.append_rope, append_fp8=_binding.append_fp8,
+                               decode_fp8=_binding.decode_fp8)
     return _ext
 
 

@@ -12,6 +12,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 from pathlib import Path
 
 PKG = Path(__file__).resolve().parent
@@ -42,12 +43,20 @@ def command(out: Path = LIB, verbose_ptxas: bool = False) -> list[str]:
     return cmd + ["-o", str(out), *map(str, SOURCES)]
 
 
+def binding_tag() -> str:
+    """What an extension has to be built against to be used here."""
+    import torch
+
+    return f"torch {torch.__version__}, python {sys.version_info.major}.{sys.version_info.minor}"
+
+
 def binding_command(out: Path = BINDING) -> list[str]:
     import torch
 
     torch_dir = Path(torch.__file__).resolve().parent
     cuda = Path(nvcc()).resolve().parent.parent
     return ["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            f'-DPKV_BUILT_FOR="{binding_tag()}"',
             "-I", str(ROOT / "include"), "-I", sysconfig.get_paths()["include"], "-I", str(torch_dir / "include"),
             "-I", str(cuda / "include"), "-o", str(out), str(BINDING_SOURCES[0]), "-L", str(torch_dir / "lib"),
             f"-Wl,-rpath,{torch_dir / 'lib'}", "-ltorch_python", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda"]
@@ -60,11 +69,24 @@ def stale(out: Path = LIB, sources=None) -> bool:
     return any(p.stat().st_mtime > t for p in (SOURCES + HEADERS if sources is None else sources))
 
 
+def build_binding(force: bool = False) -> bool:
+    """The package runs without the extension (its calls then go through ctypes):
+    where it cannot be built here, that is a warning, and none is left from another time."""
+    if not force and not stale(BINDING, BINDING_SOURCES) and binding_tag().encode() in BINDING.read_bytes():
+        return True
+    try:
+        subprocess.run(binding_command(BINDING), check=True)
+        return True
+    except (OSError, subprocess.CalledProcessError) as e:
+        BINDING.unlink(missing_ok=True)
+        warnings.warn(f"{BINDING.name} was not built, calls go through ctypes: {e}", stacklevel=2)
+        return False
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> Path:
     if force or stale():
         subprocess.run(command(verbose_ptxas=verbose_ptxas), check=True)
-    if force or stale(BINDING, BINDING_SOURCES):
-        subprocess.run(binding_command(), check=True)
+    build_binding(force)
     return LIB
 
 
