@@ -534,7 +534,8 @@ pkv_status paged_attention_decode_int8(const void* q, const uint8_t* kv_cache, c
  * with paged_kv_append's slot rules (a padding token's query is rotated all
  * the same).  Each product and each sum is rounded to fp32, the result once to
  * the dtype.  A position outside [0, max_positions) sets PKV_DEVERR_POSITION:
- * that token's q_out and cache rows are left as they were.
+ * that token's q_out and cache rows are left as they were (so a q_out that was
+ * allocated for the call holds nothing defined there).
  *
  *   q, k, v      : device, heads [n_heads][head_dim] of one token contiguous;
  *                  token i starts at element i * {q,k,v}_stride, so that views
@@ -586,7 +587,9 @@ pkv_status paged_kv_append_rope(const void* q, int64_t q_stride, const void* k, 
  * are); of two with the same slot the last counts.  A block whose tokens come
  * in two places of one call is undefined.
  *
- *   k, v : device, f32, f16 or bf16 (`dtype`), strides as paged_kv_append_rope
+ *   k, v      : device, f32, f16 or bf16 (`dtype`), strides as paged_kv_append_rope
+ *   kv_scales : of a block that goes on (T without its offset 0): a power of two in
+ *               that range, as these calls leave it
  */
 pkv_status paged_kv_append_fp8(const void* k, int64_t k_stride, const void* v, int64_t v_stride, pkv_dtype dtype,
                                const int64_t* slot_mapping, int32_t num_tokens, uint8_t* kv_cache, float* kv_scales,
@@ -617,8 +620,12 @@ pkv_status paged_kv_copy_blocks_fp8(uint8_t* kv_cache, float* kv_scales, const i
  *   num_blocks: with num_blocks * n_kv_heads < 2^31
  *   q_len     : 1 .. 16, the last tokens of every context; query i sees tokens
  *               j < context_lens[b] - q_len + i + 1
- *   kv_scales : of the blocks read: positive and normal, as the appends write
- *               them (any such value, not only powers of two)
+ *   kv_scales : of the blocks read: from 2^-48 to below 2^49, the appends' range
+ *               (any value in it, not only powers of two).  Weights are held
+ *               in f16 times V's scale, relative to the row's largest such
+ *               product (f16 data: with a remainder): a token whose product is
+ *               2^21 times smaller than that keeps fewer bits of its weight,
+ *               one 2^32 times smaller counts in the softmax's sum alone
  *   workspace : paged_attention_fp8_workspace_size() bytes on the current
  *               device, 256-byte aligned, for one call at a time.  It may hold
  *               anything (no clearing, no state from call to call) and serves

@@ -754,7 +754,8 @@ def paged_kv_append_rope(k, v, positions, cos_sin, slot_mapping, k_cache, v_cach
     ``interleaved``.  ``k``, ``v`` and ``q`` may be views of one packed
     projection (heads of a token contiguous).  Returns the rotated queries in
     ``q_out`` (a new tensor by default; ``q_out=q`` rotates in place), or None
-    without ``q``."""
+    without ``q``.  A position outside the table sets DEVERR_POSITION and leaves
+    its token's rows as they were: in a new tensor they are not initialised."""
     if stream is None and block_size == 16 and (quick := _ext or _quick()):
         done = quick.append_rope(k, v, positions, cos_sin, slot_mapping, k_cache, v_cache, q, q_out, interleaved, False)
         if done is not NotImplemented:
@@ -788,8 +789,11 @@ def _fp8_shape(kv_cache, kv_scales, block_size: int):
 def paged_kv_append_fp8(k, v, slot_mapping, kv_cache, kv_scales, block_size: int = 16, stream=None) -> None:
     """Quantise ``k[i]``, ``v[i]`` into slot ``slot_mapping[i]`` of the FP8 cache
     (in place): e4m3 codes with one power-of-two scale for each block, kv head
-    and K or V, which grows with what is appended (its rules, and which tokens
-    of a call have to be consecutive, in include/pagedkv.h)."""
+    and K or V, which grows with what is appended; offset 0 starts a block anew
+    (the rules in include/pagedkv.h).  The tokens of one block have to stand
+    together in the call, with no padding between them: a block whose tokens
+    come in two places of one call is undefined, and nothing reports it (flatten
+    drafts sequence by sequence)."""
     if stream is None and block_size == 16 and (quick := _ext or _quick()):
         if quick.append_fp8(k, v, slot_mapping, kv_cache, kv_scales) is not NotImplemented:
             return
@@ -805,7 +809,8 @@ def paged_kv_append_fp8(k, v, slot_mapping, kv_cache, kv_scales, block_size: int
 def paged_kv_append_rope_fp8(k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales, q=None, q_out=None,
                              interleaved: bool = False, block_size: int = 16, stream=None):
     """paged_kv_append_rope into the FP8 cache (keys are quantised from their
-    fp32 rotation); returns the rotated queries as there."""
+    fp32 rotation); returns the rotated queries as there.  A block's tokens have
+    to stand together in the call, as for paged_kv_append_fp8."""
     if stream is None and block_size == 16 and (quick := _ext or _quick()):
         done = quick.append_rope(k, v, positions, cos_sin, slot_mapping, kv_cache, kv_scales, q, q_out, interleaved, True)
         if done is not NotImplemented:

@@ -421,7 +421,7 @@ __device__ __forceinline__ void append_f8_rows(const AppendF8Params& p, int64_t 
   }
   const float need = f8_scale_for(amax);
   const float s_new = fresh ? need : fmaxf(s_old, need);
-  const float inv = 1.0f / s_new;  // exact: a power of two
+  const float inv = 1.0f / s_new;  // exact: a power of two, if the block's old scale is one
   uint8_t* tile = p.kv + block_head * f8_tile_bytes(D) + (is_v ? kBlockTokens * D : 0);
   const bool regrid = !fresh && s_new != s_old;
 #pragma unroll

@@ -297,6 +297,19 @@ def test_decode_scales_that_are_no_powers_of_two_and_negative_scale():
     check_decode(tuple(case))
 
 
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("v_scales", [(2.0 ** -48,), (2.0 ** 48 * 1.9375,), (2.0 ** -48, 2.0 ** 48 * 1.9375), (2.0 ** 48, 1.0, 2.0 ** -48)])
+@pytest.mark.parametrize("q_len", [1, 3])
+def test_decode_scales_at_the_ends_of_their_range(dtype, v_scales, q_len):
+    """V's scales at one end, or both in turn: weights and their sum are formed from them."""
+    q, kv, scales, tables, lens, scale = decode_case([700, 90, 3000, 17], 8, 2, 128, dtype, seed=66, q_len=q_len)
+    scales[..., 1] = torch.tensor(v_scales, device="cuda").repeat(len(scales) // len(v_scales) + 1)[: len(scales), None]
+    for k_scale in (2.0 ** -48, 2.0 ** 48 * 1.9375):  # the scores stay what they are
+        at = scales.clone()
+        at[..., 0] = k_scale
+        check_decode((q, kv, at, tables, lens, scale * 2.0 ** -8 / k_scale))
+
+
 def test_decode_nan_and_infinite_inputs_reach_only_their_rows():
     case = decode_case([70, 70], 8, 2, 64, torch.float16, seed=34)
     q, kv, scales, tables, lens, _ = case
