@@ -109,6 +109,50 @@ def test_an_input_that_the_kernel_in_front_writes_last(call, late, captured):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("call,late", [(append_rope, "slots"), (append_fp8, "v"), (append_rope_fp8, "pos"), (decode, "lens"),
+                                       (decode, "codes")])
+def test_an_input_from_another_stream(call, late, captured):
+    """The input is summed up on another stream; a short kernel and the wait for that stream stand in front of the call."""
+    inputs = Inputs()
+    want = [x.clone() for x in call(inputs.copies())]
+    t = inputs.copies()
+    value = t[late].clone()
+    terms = torch.zeros((value.numel(), (1 << 30) // (value.numel() * value.element_size())), dtype=value.dtype, device="cuda")
+    terms[:, 0] = value.flatten()
+    side, short = torch.cuda.Stream(), torch.zeros(8, device="cuda")
+
+    def both():
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            torch.sum(terms, 1, dtype=value.dtype, out=t[late].view(-1))
+        short.add_(1)
+        main.wait_stream(side)
+        return call(t)
+
+    both()
+    torch.cuda.synchronize()
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = both()
+    for _ in range(3):
+        for n, x in inputs.t.items():
+            t[n].copy_(x)
+        t[late].fill_(inputs.before.get(late, 0))
+        torch.cuda.synchronize()
+        if captured:
+            graph.replay()
+        else:
+            got = both()
+        torch.cuda.synchronize()
+        for x, y in zip(got, want, strict=True):
+            assert torch.equal(x, y)
+    assert pkv.pkv_get_device_error() == 0
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("call", ["append_rope", "append_fp8", "append_rope_fp8", "decode", "decode_workspace", "decode_16"])
 def test_a_launch_that_fails_is_that_calls_error_alone(call):
     """A call on a stream whose capture was given up fails; the next call, elsewhere, does not."""
