@@ -108,7 +108,10 @@ pkv_status append_f8(const RopeAppendParams& rp, pkv_dtype dtype, uint8_t* kv_ca
   // A token a pair of warps while all of them fit the device at once (a decode
   // step: every token its own run); else 16, so that a prompt's warps are not
   // mostly ones without a run start.  (64 single tokens, 32/8 heads: 4.3 us,
-  // 36.7 with 16; 16384 prompt tokens, 8 heads: 20.8 us, 117 with one.)
+  // 36.7 with 16; 16384 prompt tokens, 8 heads: 20.8 us, 117 with one.)  Steps of
+  // many sequences come out on the wrong side of it, 16 runs behind one another
+  // in a pair: 310 single tokens, 8 heads, 37.8 us, 9.9 with one; 512, 37.3, 14.3;
+  // 256, 32 heads, 40.9, 23.3; at 4096, 8 heads, 66.5, 105.5.
   p.tokens_per_pair = static_cast<int64_t>(rp.num_tokens) * rp.n_kv <= static_cast<int64_t>(di.sm_count) * 16 ? 1 : 16;
   p.token_chunks = (rp.num_tokens + p.tokens_per_pair - 1) / p.tokens_per_pair;
   const int64_t items = static_cast<int64_t>(p.token_chunks) * rp.n_kv * (p.tokens_per_pair == 1 ? 2 : 1);
