@@ -137,9 +137,9 @@ __device__ __forceinline__ unsigned long long load_relaxed(const unsigned long l
 }
 
 // Sets a word of the arrivals to 0 unless it holds some of this call's n already
-// (j `arrival`, j < n).  `word` is what it held when last read.  Every CTA does this in front of its own arrival, so that
-// none is counted on top of, or lost with, what was there before the call: a workspace
-// needs no clearing.
+// (j `arrival`, j < n).  `word` is what it held when last read.  Every CTA does this
+// in front of its own arrival, so that none is counted on top of, or lost with, what
+// was there before the call: a workspace needs no clearing.
 __device__ __forceinline__ void f8_settle(unsigned long long* at, unsigned long long word, unsigned long long arrival,
                                           int n) {
   while (true) {
@@ -859,7 +859,7 @@ __global__ void __launch_bounds__(f8_warps(NR) * 32, 1)
       }
     };
     // The next tiles into n slots from `slot` on, a lane for each.
-    const int withhold_at = unit_begin(sc, p.withhold_unit);
+    const int withhold_at = p.withhold_unit < sc.U ? unit_begin(sc, p.withhold_unit) : -1;
     const int withheld = withhold_at >= k0 && withhold_at < k1 ? 0 : -1;  // which of the unit's tiles
     int issued = 0;
     auto issue = [&](int slot, int n) {

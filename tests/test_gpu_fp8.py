@@ -486,6 +486,13 @@ def test_decode_wait_that_runs_out_and_the_next_call(lens, n_q, n_kv, d, q_len, 
     assert pkv.pkv_get_device_error() == 0
 
 
+@pytest.mark.parametrize("unit", [2368, 1 << 20, (1 << 31) - 2])
+def test_decode_withheld_unit_that_is_none(unit):
+    case = decode_case([20000, 40], 4, 1, 128, torch.bfloat16, seed=67)
+    assert torch.equal(bits(run_decode(case, wait_limit_us=5000, test_withhold_unit=unit)), bits(check_decode(case)))
+    assert pkv.pkv_get_device_error() == 0
+
+
 def test_two_graphs_share_a_workspace_in_turn():
     cases = [decode_case([2500, 40], 8, 2, 128, torch.bfloat16, seed=47), decode_case([300] * 9, 16, 1, 64, torch.float16, seed=48)]
     want = [run_decode(c) for c in cases]
